@@ -1,5 +1,6 @@
 /*
- * ck.h -- C ABI of the MI355X (gfx950) ConvRot INT8 linear and SwiGLU MLP.
+ * ck.h -- C ABI of the MI355X (gfx950) ConvRot INT8 linear and SwiGLU MLP, and
+ * of the attention-side operators between such linears.
  *
  * What the library computes (sources cited by page title and section):
  *
@@ -332,6 +333,97 @@ ck_status ck_swiglu_mlp_w8a16(const uint16_t *x, const int8_t *w_gu, const float
                               int64_t i, int32_t group, uint16_t *y, void *workspace,
                               size_t workspace_bytes, void *stream);
 size_t ck_swiglu_mlp_w8a16_workspace_size(int64_t m, int64_t h, int64_t i);
+
+/* ---- Attention side of a block: per-head norms with rotation, cross attention ----
+ * The operators between the q / kv projections (ck_int8_linear) and the output
+ * projection.  Heads are 16-bit values (BF16, the linears' type, or FP16) in
+ * [batch, tokens, heads, d] with a stride for each of the first three
+ * dimensions, so q, k and v may be column ranges of packed projection outputs.
+ * d is a multiple of 8, strides are multiples of 8 elements in [0, 2^23)
+ * (token and head) or [0, 2^40) (batch) and data is 16-byte aligned. */
+typedef enum ck_dtype {
+    CK_DTYPE_BF16 = 0,
+    CK_DTYPE_FP16 = 1
+} ck_dtype;
+
+typedef struct ck_heads {
+    void *data;                /* 16-byte aligned                              */
+    int64_t batch_stride;      /* in elements                                  */
+    int64_t token_stride;
+    int64_t head_stride;
+} ck_heads;
+
+/* Which channels the position rotation turns together: (i, i + rot / 2) or
+ * (2 i, 2 i + 1). */
+typedef enum ck_pairing {
+    CK_PAIR_HALF = 0,
+    CK_PAIR_INTERLEAVED = 1
+} ck_pairing;
+
+/* One side (the queries or the keys) of ck_qk_norm_rope. */
+typedef struct ck_qk_side {
+    ck_heads x;                /* [batch, tokens, heads, d], read               */
+    ck_heads y;                /* the same shape, written; may be x itself (the
+                                  same data and strides), must not otherwise
+                                  overlap anything read                         */
+    int64_t batch, tokens, heads;
+    const float *weight;       /* [d] FP32, 16-byte aligned, or NULL (ones)     */
+    const float *cos, *sin;    /* [table_rows, rot / 2] FP32, 16-byte aligned;
+                                  both NULL: this side is not rotated           */
+    int64_t table_rows;
+    const int32_t *pos;        /* [batch, tokens], the token's table row, rows
+                                  pos_stride apart; NULL: row t for token t     */
+    int64_t pos_stride;
+} ck_qk_side;
+
+/* RMS norm of every query and key head and the position rotation, one launch:
+ *   z = x * rsqrt(mean(x^2) + eps) * weight     over the d channels of a head
+ *   y[a] = z[a] cos - z[b] sin, y[b] = z[b] cos + z[a] sin   for the pairs
+ *   (a, b) of the first rot channels; y = z for the others
+ * in FP32, rounded once.  k may be NULL (one side only); an empty side (batch,
+ * tokens or heads 0) is skipped, its pointers unread.
+ *   d    multiple of 8, at most 256;  rot in [0, d], a multiple of 16 (half) or
+ *        8 (interleaved); rot == 0 rotates neither side
+ *   eps  finite, at least 2^-126
+ * A position outside [0, table_rows) gives NaN in that token's heads; without
+ * pos, tokens <= table_rows.
+ * Errors: CK_EINVAL on null or misaligned pointers, unknown type or pairing,
+ * eps; CK_ESHAPE on sizes and strides; CK_EUNSUPPORTED on d > 256 or a side of
+ * 2^31 or more heads. */
+ck_status ck_qk_norm_rope(const ck_qk_side *q, const ck_qk_side *k, int64_t d, int64_t rot,
+                          int32_t pairing, int32_t dtype, float eps, void *stream);
+
+/* Attention over encoder states of another length:
+ *   o[b, t, h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q[b, t, h] . k_j),
+ * j over the allowed keys of encoder sequence b / (batch / kv_batch) and key
+ * head h / (heads / kv_heads).
+ *   q, o      [batch, tq, heads, d]; o must not overlap what is read
+ *   k, v      [kv_batch, tk, kv_heads, d]; batch % kv_batch == 0 (consecutive
+ *             sequences share an encoder sequence: beams, samples of a prompt)
+ *             and heads % kv_heads == 0
+ *   d         multiple of 8, at most 128;  tq, tk >= 0, below 2^31
+ *   scale     finite, > 0
+ *   kv_len    [kv_batch] int32, the keys of each encoder sequence (taken into
+ *             [0, tk]), or NULL
+ *   key_mask  [kv_batch, tk] bytes, rows mask_stride apart, 0 = not allowed, or
+ *             NULL
+ * A row with no allowed key is zero.  Keys and values that are not allowed are
+ * not read (NaN and infinities there have no effect).  Scores, the softmax and
+ * the sums are FP32; p is rounded to the data's type for the second product
+ * (the matrix cores' operand), and o once.  The result does not depend on
+ * timing (fixed order of sums).
+ *   workspace  ck_cross_attn_workspace_size(...) bytes (0: may be NULL),
+ *              256-byte aligned, clobbered
+ * Errors: CK_EINVAL on null or misaligned pointers, unknown type, scale;
+ * CK_ESHAPE on sizes and strides; CK_EUNSUPPORTED on d > 128 or 2^31 or more
+ * rows or key heads; CK_EWORKSPACE. */
+ck_status ck_cross_attn(const ck_heads *q, const ck_heads *k, const ck_heads *v, const ck_heads *o,
+                        int64_t batch, int64_t kv_batch, int64_t tq, int64_t tk, int64_t heads,
+                        int64_t kv_heads, int64_t d, int32_t dtype, float scale,
+                        const int32_t *kv_len, const uint8_t *key_mask, int64_t mask_stride,
+                        void *workspace, size_t workspace_bytes, void *stream);
+size_t ck_cross_attn_workspace_size(int64_t batch, int64_t kv_batch, int64_t tq, int64_t tk,
+                                    int64_t heads, int64_t kv_heads, int64_t d);
 
 /* ---- test hooks: the same device code with its intermediate exposed ---- */
 

@@ -21,6 +21,11 @@ Entry points keep the C names:
 * W8A16 (BF16 activations, INT8 weights in the blocked layout):
   ``ck_act_rotate_bf16``, ``ck_w8a16_gemm_bf16``, ``ck_int8_linear_w8a16``,
   ``ck_swiglu_mlp_w8a16``
+* attention side (BF16 or FP16 heads ``[batch, tokens, heads, d]``, strided
+  views such as column ranges of packed projections included):
+  ``ck_qk_norm_rope(q, k=None, q_weight, k_weight, q_rope, k_rope, ...)``: per-head
+  RMS norm and position rotation; ``ck_cross_attn(q, k, v, scale, kv_len,
+  key_mask, ...)``: attention over encoder states of another length
 * test hooks ``ck_int8_gemm_i32``, ``ck_w8a16_gemm_f32``, ``ck_silu_f32``, ``ck_act_rotate_f32``
 
 INT8 operand layouts, each with its own tensor form so that a call can tell
@@ -53,6 +58,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libck_convrot.so")
@@ -105,6 +111,9 @@ def bind(path: str) -> ctypes.CDLL:
         "ck_w8a16_gemm_f32": [p, p, i64, i64, i64, p, p],
         "ck_int8_linear_w8a16": [p, i64, i32, p, p, p, p, i64, i64, i64, i32, p, p, sz, p],
         "ck_swiglu_mlp_w8a16": [p, p, p, p, p, i64, i64, i64, i32, p, p, sz, p],
+        "ck_qk_norm_rope": [p, p, i64, i64, i32, i32, ctypes.c_float, p],
+        "ck_cross_attn": [p, p, p, p, i64, i64, i64, i64, i64, i64, i64, i32, ctypes.c_float,
+                          p, p, i64, p, sz, p],
         "ck_silu_f32": [p, i64, p, p],
         "ck_act_rotate_f32": [p, i64, i64, i64, i32, i32, p, p],
         "ck_probe_mfma_i8": [p, i64, i32, p, p],
@@ -122,6 +131,8 @@ def bind(path: str) -> ctypes.CDLL:
     L.ck_swiglu_mlp_w8a16_workspace_size.restype = sz
     L.ck_swiglu_mlp_workspace_size.argtypes = [i64, i64, i64]
     L.ck_swiglu_mlp_workspace_size.restype = sz
+    L.ck_cross_attn_workspace_size.argtypes = [i64] * 7
+    L.ck_cross_attn_workspace_size.restype = sz
     L.ck_probe_mfma_workgroups.argtypes = []
     L.ck_probe_mfma_workgroups.restype = i64
     L.ck_noalloc_scratch_bytes.argtypes = []
@@ -654,6 +665,209 @@ def ck_swiglu_mlp_w8a16(x, w_gu, s_gu, w_down, s_down, group: int = 128, out=Non
     return y
 
 
+# ---------------------------------------------------------------------------
+# Attention side: per-head norms with rotation, cross attention
+# ---------------------------------------------------------------------------
+CK_DTYPE_BF16, CK_DTYPE_FP16 = 0, 1
+CK_PAIR_HALF, CK_PAIR_INTERLEAVED = 0, 1
+_PAIRING = {"half": CK_PAIR_HALF, "interleaved": CK_PAIR_INTERLEAVED}
+# ck_heads and ck_qk_side of include/ck.h as packed 8-byte words (bytes pass as
+# their address)
+_PACK_HEADS, _PACK_SIDE = struct.Struct("4Q"), struct.Struct("17Q")
+
+
+def _heads(t, what, dtype=None, dev=None):
+    """Check a [batch, tokens, heads, d] tensor of 16-bit values; returns the
+    words of its ck_heads (address, batch, token and head strides)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{what} must be a torch.Tensor")
+    if t.device.type != "cuda" or (dev is not None and t.device != dev):
+        raise ValueError(f"{what} must be on {dev or 'a GPU'}, got {t.device}")
+    if t.dtype not in (torch.bfloat16, torch.float16) or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{what} needs dtype {dtype or 'bfloat16 or float16'}, got {t.dtype}")
+    if t.dim() != 4:
+        raise ValueError(f"{what} needs [batch, tokens, heads, d], got shape {tuple(t.shape)}")
+    sizes, strides = t.shape, t.stride()
+    if sizes[3] < 8 or sizes[3] % 8:
+        raise ValueError(f"{what}: the head size must be a multiple of 8, got {sizes[3]}")
+    if strides[3] != 1:
+        raise ValueError(f"{what}: the channels of a head must be contiguous")
+    # the stride of a dimension of one element is never used
+    words = [t.data_ptr()] + [st if n > 1 else 0 for n, st in zip(sizes[:3], strides)]
+    if words[0] % 16 or any(w % 8 for w in words[1:]):
+        raise ValueError(f"{what} needs 16-byte aligned heads (strides in multiples of 8 elements)")
+    return words
+
+
+def _view_span(t):
+    """Byte range [a, b) that a strided tensor lies in."""
+    n = sum((s - 1) * st for s, st in zip(t.shape, t.stride())) + 1 if t.numel() else 0
+    return t.data_ptr(), t.data_ptr() + n * t.element_size()
+
+
+def _disjoint(a, b):
+    """Whether two [batch, tokens, heads, d] views share no element: apart in
+    memory, or different column ranges of rows with the same pitch."""
+    (a0, a1), (b0, b1) = _view_span(a), _view_span(b)
+    if a1 <= b0 or b1 <= a0:
+        return True
+    pitch = a.stride(1)
+    if a.shape[1] < 2 or b.shape[1] < 2 or b.stride(1) != pitch:
+        return False
+    for t in (a, b):   # one pitch over all (batch, token) rows
+        if t.shape[0] > 1 and t.stride(0) % pitch:
+            return False
+    w = [(t.shape[2] - 1) * t.stride(2) + t.shape[3] for t in (a, b)]
+    gap = (b0 - a0) // a.element_size() % pitch    # b's columns start `gap` after a's
+    return w[0] <= gap and gap + w[1] <= pitch
+
+
+def _heads_out(out, shape, dtype, dev, what, reads, same=None):
+    """An output of `shape`: a new contiguous tensor, or `out` checked; it may
+    not share elements with `reads`, or else be `same` itself."""
+    import torch
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _heads(out, what, dtype, dev)
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"{what} needs shape {tuple(shape)}, got {tuple(out.shape)}")
+    for n, st in zip(out.shape, out.stride()):
+        if n > 1 and st == 0:
+            raise ValueError(f"{what} must not be an expanded tensor")
+    for t in reads:
+        if t is None or (t is same and t.data_ptr() == out.data_ptr() and t.stride() == out.stride()):
+            continue
+        if not _disjoint(out, t):
+            raise ValueError(f"{what} must not share memory with what the call reads")
+    return out
+
+
+def _qk_side(x, y, weight, rope, pos, what, d, dev):
+    """The words of one side's ck_qk_side (include/ck.h)."""
+    import torch
+    b, t, h = x.shape[:3]
+    words = _heads(x, what, None, dev) + _heads(y, what + "_out", x.dtype, dev) + [b, t, h]
+    if weight is not None:
+        _need(weight, torch.float32, 1, what + "_weight")
+        if weight.shape[0] != d or weight.device != dev:
+            raise ValueError(f"{what}_weight needs a ({d},) tensor on {dev}")
+    words.append(weight.data_ptr() if weight is not None else 0)
+    if rope is None:
+        if pos is not None:
+            raise ValueError(f"{what}_pos without {what}_rope")
+        return words + [0, 0, 0, 0, 0]
+    cos, sin = rope
+    for name, tab in (("cos", cos), ("sin", sin)):
+        _need(tab, torch.float32, 2, f"{what}_rope {name}")
+        if tab.shape != cos.shape or tab.device != dev:
+            raise ValueError(f"{what}_rope needs cos and sin of one shape on {dev}")
+    words += [cos.data_ptr(), sin.data_ptr(), cos.shape[0]]
+    if pos is None:
+        if t > cos.shape[0]:
+            raise ValueError(f"{what}_rope has {cos.shape[0]} rows for {t} tokens")
+        return words + [0, 0]
+    if (not isinstance(pos, torch.Tensor) or pos.dtype != torch.int32 or pos.device != dev
+            or tuple(pos.shape) != (b, t) or (t > 1 and pos.stride(1) != 1)):
+        raise ValueError(f"{what}_pos needs an int32 ({b}, {t}) tensor with contiguous rows on {dev}")
+    return words + [pos.data_ptr(), pos.stride(0) if b > 1 else 0]
+
+
+def ck_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, q_rope=None, k_rope=None, q_pos=None,
+                    k_pos=None, pairing="half", eps: float = 1e-6, q_out=None, k_out=None):
+    """RMS norm of every head of q (and k) over its channels, times the FP32
+    weight [d], and the position rotation, in one launch.
+
+    q [batch, tokens, heads, d], k likewise with its own sizes (same d and
+    dtype).  q_rope / k_rope: (cos, sin), FP32 [rows, rot / 2] each, or None (no
+    rotation on that side); row t for token t, or row pos[b, t] with int32
+    q_pos / k_pos (a position outside the table gives NaN in that token).
+    pairing "half" turns channels (i, i + rot / 2), "interleaved" (2 i, 2 i + 1).
+    Outputs are new contiguous tensors, or q_out / k_out, which may be q / k
+    themselves.  Returns q_out, or (q_out, k_out) when k is given."""
+    if pairing not in _PAIRING:
+        raise ValueError(f"unknown pairing {pairing!r}")
+    _heads(q, "q")
+    dev, d = q.device, q.shape[3]
+    rot = 0
+    for rope in (q_rope, k_rope):
+        if rope is None:
+            continue
+        if not isinstance(rope, (tuple, list)) or len(rope) != 2:
+            raise ValueError("a rope is (cos, sin)")
+        r = 2 * rope[0].shape[-1]
+        if rot and r != rot:
+            raise ValueError("q_rope and k_rope turn different numbers of channels")
+        rot = r
+    step = 16 if pairing == "half" else 8
+    if rot > d or rot % step:
+        raise ValueError(f"the rotated channels must be a multiple of {step} up to {d}, got {rot}")
+    if d > 256:
+        raise ValueError(f"head size {d} is over 256")
+    if k is None and not (k_weight is None and k_rope is None and k_pos is None and k_out is None):
+        raise ValueError("arguments for k without k")
+    y = _heads_out(q_out, q.shape, q.dtype, dev, "q_out", (q, k), q)
+    side_q = _PACK_SIDE.pack(*_qk_side(q, y, q_weight, q_rope, q_pos, "q", d, dev))
+    side_k = z = None
+    if k is not None:
+        _heads(k, "k", q.dtype, dev)
+        if k.shape[3] != d:
+            raise ValueError(f"q and k need one head size, got {d} and {k.shape[3]}")
+        z = _heads_out(k_out, k.shape, q.dtype, dev, "k_out", (q, k), k)
+        if q_out is not None and k_out is not None and not _disjoint(y, z):
+            raise ValueError("q_out and k_out must not share memory")
+        side_k = _PACK_SIDE.pack(*_qk_side(k, z, k_weight, k_rope, k_pos, "k", d, dev))
+    import torch
+    _call("ck_qk_norm_rope", side_q, side_k, d, rot, _PAIRING[pairing],
+          CK_DTYPE_FP16 if q.dtype == torch.float16 else CK_DTYPE_BF16, eps, _stream(q))
+    return y if k is None else (y, z)
+
+
+def ck_cross_attn(q, k, v, scale=None, kv_len=None, key_mask=None, out=None, workspace=None):
+    """softmax(scale q k^T) v over encoder states of another length.
+
+    q [batch, tq, heads, d]; k, v [kv_batch, tk, kv_heads, d] with batch a
+    multiple of kv_batch (consecutive sequences share an encoder sequence) and
+    heads a multiple of kv_heads; d a multiple of 8 up to 128.  scale: d ** -0.5
+    by default.  kv_len int32 [kv_batch]: the keys of each encoder sequence;
+    key_mask bool or uint8 [kv_batch, tk]: False / 0 keys are left out.  What is
+    left out is not read; a row with no key is zero.
+    Returns [batch, tq, heads, d], contiguous unless `out` is given."""
+    import torch
+    hq = _heads(q, "q")
+    dev, (b, tq, h, d) = q.device, q.shape
+    hk, hv = _heads(k, "k", q.dtype, dev), _heads(v, "v", q.dtype, dev)
+    kb, tk, kh, dk = k.shape
+    if tuple(v.shape) != (kb, tk, kh, dk):
+        raise ValueError(f"k and v need one shape, got {tuple(k.shape)} and {tuple(v.shape)}")
+    if dk != d or d > 128:
+        raise ValueError(f"q and k need one head size up to 128, got {d} and {dk}")
+    if b and tq and h and (not kb or b % kb or not kh or h % kh):
+        raise ValueError(f"batch {b} and heads {h} must be multiples of the encoder's {kb} and {kh}")
+    scale = d ** -0.5 if scale is None else float(scale)
+    if not 0.0 < scale < 3.4e38:
+        raise ValueError(f"scale must be positive and finite, got {scale}")
+    if kv_len is not None:
+        _need(kv_len, torch.int32, 1, "kv_len")
+        if kv_len.shape[0] != kb or kv_len.device != dev:
+            raise ValueError(f"kv_len needs ({kb},) on {dev}")
+    stride = 0
+    if key_mask is not None:
+        if (not isinstance(key_mask, torch.Tensor) or key_mask.dtype not in (torch.bool, torch.uint8)
+                or key_mask.device != dev or tuple(key_mask.shape) != (kb, tk)
+                or (tk > 1 and key_mask.stride(1) != 1)):
+            raise ValueError(f"key_mask needs a bool or uint8 ({kb}, {tk}) tensor with contiguous rows on {dev}")
+        stride = key_mask.stride(0) if kb > 1 else 0
+    y = _heads_out(out, q.shape, q.dtype, dev, "out", (q, k, v))
+    need = lib().ck_cross_attn_workspace_size(b, kb, tq, tk, h, kh, d)
+    ws = _workspace(workspace, need, dev) if need else None
+    pack = _PACK_HEADS.pack
+    _call("ck_cross_attn", pack(*hq), pack(*hk), pack(*hv), pack(*_heads(y, "out")), b, kb, tq, tk, h, kh, d,
+          CK_DTYPE_FP16 if q.dtype == torch.float16 else CK_DTYPE_BF16, scale, _ptr(kv_len), _ptr(key_mask),
+          stride, _ptr(ws), ws.numel() if need else 0, _stream(q))
+    return y
+
+
 def ck_silu_f32(gate):
     import torch
     if gate.dtype != torch.bfloat16 or gate.device.type != "cuda" or not gate.is_contiguous():
@@ -683,3 +897,5 @@ act_quant = ck_act_quant
 int8_linear = ck_int8_linear
 int8_gemm_bf16 = ck_int8_gemm_bf16
 swiglu_mlp = ck_swiglu_mlp
+qk_norm_rope = ck_qk_norm_rope
+cross_attn = ck_cross_attn

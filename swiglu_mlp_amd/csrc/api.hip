@@ -568,4 +568,131 @@ ck_status ck_probe_stream_rows(const void* src, int64_t ld_bytes, int64_t m, int
     return from_hip(ck::launch_probe_stream(src, ld_bytes, m, read_bytes, write_bytes, dst, (hipStream_t)stream));
 }
 
+// ---- attention side ----
+
+static ck_status check_heads(const ck_heads& h)
+{
+    if (!h.data || !aligned16(h.data)) return CK_EINVAL;
+    for (const int64_t st : {h.token_stride, h.head_stride})
+        if (st < 0 || st >= (1 << 23) || st % 8 != 0) return CK_ESHAPE;
+    if (h.batch_stride < 0 || h.batch_stride >= (1LL << 40) || h.batch_stride % 8 != 0) return CK_ESHAPE;
+    return CK_OK;
+}
+
+// a * b * c of non-negative sizes, or limit if it is not below it.
+static int64_t product_below(int64_t a, int64_t b, int64_t c, int64_t limit)
+{
+    if (a == 0 || b == 0 || c == 0) return 0;
+    if (a >= limit || b >= limit || c >= limit || a * b >= limit) return limit;
+    return a * b * c < limit ? a * b * c : limit;
+}
+
+constexpr int64_t kMaxRows = 0x7fffffffLL;
+
+static ck_status check_qk_side(const ck_qk_side& s, int64_t rot, ck::QkSideArgs* out)
+{
+    *out = ck::QkSideArgs{};
+    if (s.batch < 0 || s.tokens < 0 || s.heads < 0) return CK_ESHAPE;
+    const int64_t rows = product_below(s.batch, s.tokens, s.heads, kMaxRows);
+    if (rows >= kMaxRows) return CK_EUNSUPPORTED;
+    if (rows == 0) return CK_OK;
+    CK_TRY(check_heads(s.x));
+    CK_TRY(check_heads(s.y));
+    if (s.weight && !aligned16(s.weight)) return CK_EINVAL;
+    const bool rope = rot > 0 && (s.cos || s.sin);
+    if (rope) {
+        if (!s.cos || !s.sin || !aligned16(s.cos) || !aligned16(s.sin)) return CK_EINVAL;
+        if (s.table_rows < 1 || s.table_rows > kMaxRows) return CK_ESHAPE;
+        if (s.pos ? s.pos_stride < 0 : s.tokens > s.table_rows) return CK_ESHAPE;
+        if (s.pos && ((uintptr_t)s.pos & 3u)) return CK_EINVAL;
+    }
+    out->x = static_cast<const uint16_t*>(s.x.data);
+    out->y = static_cast<uint16_t*>(s.y.data);
+    out->x_sb = s.x.batch_stride, out->x_st = s.x.token_stride, out->x_sh = s.x.head_stride;
+    out->y_sb = s.y.batch_stride, out->y_st = s.y.token_stride, out->y_sh = s.y.head_stride;
+    out->batch = s.batch, out->tokens = s.tokens, out->heads = s.heads;
+    out->w = s.weight;
+    if (rope) {
+        out->cos = s.cos, out->sin = s.sin, out->table = s.table_rows;
+        out->pos = s.pos, out->pos_sb = s.pos_stride;
+    }
+    return CK_OK;
+}
+
+ck_status ck_qk_norm_rope(const ck_qk_side* q, const ck_qk_side* k, int64_t d, int64_t rot, int32_t pairing,
+                          int32_t dtype, float eps, void* stream)
+{
+    if (!q) return CK_EINVAL;
+    if (pairing != CK_PAIR_HALF && pairing != CK_PAIR_INTERLEAVED) return CK_EINVAL;
+    if (dtype != CK_DTYPE_BF16 && dtype != CK_DTYPE_FP16) return CK_EINVAL;
+    if (!(eps >= 0x1p-126f) || eps > 3.4028235e38f) return CK_EINVAL;
+    if (d < 8 || d % 8 != 0) return CK_ESHAPE;
+    if (d > 256) return CK_EUNSUPPORTED;
+    if (rot < 0 || rot > d || rot % (pairing == CK_PAIR_HALF ? 16 : 8) != 0) return CK_ESHAPE;
+    ck::QkSideArgs a, b;
+    CK_TRY(check_qk_side(*q, rot, &a));
+    CK_TRY(check_qk_side(k ? *k : ck_qk_side{}, rot, &b));
+    return from_hip(ck::launch_qk_norm_rope(a, b, d, rot, pairing == CK_PAIR_HALF, dtype == CK_DTYPE_FP16, eps,
+                                            (hipStream_t)stream));
+}
+
+// Sizes of ck_cross_attn; *rows: query rows that share one key head's keys.
+static ck_status check_attn_sizes(int64_t batch, int64_t kv_batch, int64_t tq, int64_t tk, int64_t heads,
+                                  int64_t kv_heads, int64_t d)
+{
+    if (batch < 0 || kv_batch < 0 || tq < 0 || tk < 0 || heads < 0 || kv_heads < 0) return CK_ESHAPE;
+    if (d < 8 || d % 8 != 0) return CK_ESHAPE;
+    if (d > 128) return CK_EUNSUPPORTED;
+    if (batch == 0 || tq == 0 || heads == 0) return CK_OK;
+    if (kv_batch == 0 || batch % kv_batch != 0 || kv_heads == 0 || heads % kv_heads != 0) return CK_ESHAPE;
+    if (tk > kMaxRows || product_below(batch, tq, heads, kMaxRows) >= kMaxRows) return CK_EUNSUPPORTED;
+    return CK_OK;
+}
+
+size_t ck_cross_attn_workspace_size(int64_t batch, int64_t kv_batch, int64_t tq, int64_t tk, int64_t heads,
+                                    int64_t kv_heads, int64_t d)
+{
+    if (check_attn_sizes(batch, kv_batch, tq, tk, heads, kv_heads, d) != CK_OK) return 0;
+    if (batch == 0 || tq == 0 || heads == 0 || tk == 0) return 0;
+    return round_up(ck::cross_attn_workspace(batch, kv_batch, tq, tk, heads, kv_heads, d));
+}
+
+ck_status ck_cross_attn(const ck_heads* q, const ck_heads* k, const ck_heads* v, const ck_heads* o, int64_t batch,
+                        int64_t kv_batch, int64_t tq, int64_t tk, int64_t heads, int64_t kv_heads, int64_t d,
+                        int32_t dtype, float scale, const int32_t* kv_len, const uint8_t* key_mask,
+                        int64_t mask_stride, void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (dtype != CK_DTYPE_BF16 && dtype != CK_DTYPE_FP16) return CK_EINVAL;
+    if (!(scale > 0.0f) || scale > 3.4028235e38f) return CK_EINVAL;
+    CK_TRY(check_attn_sizes(batch, kv_batch, tq, tk, heads, kv_heads, d));
+    if (batch == 0 || tq == 0 || heads == 0) return CK_OK;
+    if (!q || !o || (tk > 0 && (!k || !v))) return CK_EINVAL;
+    CK_TRY(check_heads(*q));
+    CK_TRY(check_heads(*o));
+    if (tk > 0) {
+        CK_TRY(check_heads(*k));
+        CK_TRY(check_heads(*v));
+    }
+    if (kv_len && ((uintptr_t)kv_len & 3u)) return CK_EINVAL;
+    if (key_mask && mask_stride < 0) return CK_ESHAPE;
+    const size_t need = ck_cross_attn_workspace_size(batch, kv_batch, tq, tk, heads, kv_heads, d);
+    if (need && (!workspace || workspace_bytes < need || ((uintptr_t)workspace % kAlign) != 0)) return CK_EWORKSPACE;
+    ck::AttnArgs a{};
+    const ck_heads none{};
+    const ck_heads &kk = tk > 0 ? *k : none, &vv = tk > 0 ? *v : none;
+    a.q = static_cast<const uint16_t*>(q->data), a.k = static_cast<const uint16_t*>(kk.data);
+    a.v = static_cast<const uint16_t*>(vv.data), a.o = static_cast<uint16_t*>(o->data);
+    a.q_sb = q->batch_stride, a.q_st = q->token_stride, a.q_sh = q->head_stride;
+    a.k_sb = kk.batch_stride, a.k_st = kk.token_stride, a.k_sh = kk.head_stride;
+    a.v_sb = vv.batch_stride, a.v_st = vv.token_stride, a.v_sh = vv.head_stride;
+    a.o_sb = o->batch_stride, a.o_st = o->token_stride, a.o_sh = o->head_stride;
+    a.batch = batch, a.kv_batch = kv_batch, a.tq = tq, a.tk = tk, a.heads = heads, a.kv_heads = kv_heads, a.d = d;
+    a.fp16 = dtype == CK_DTYPE_FP16;
+    a.scale = scale;
+    a.kv_len = kv_len;
+    a.mask = key_mask, a.mask_sb = mask_stride;
+    a.ws = workspace;
+    return from_hip(ck::launch_cross_attn(a, (hipStream_t)stream));
+}
+
 }  // extern "C"

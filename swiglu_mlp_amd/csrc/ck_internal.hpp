@@ -108,6 +108,48 @@ bool use_small_kernel(int64_t m, int64_t n);
 
 int num_cus();
 
+// RMS norm and position rotation of query and key heads (qknorm.hip).  One
+// side: x, y [batch, tokens, heads, d] 16-bit values with strides in elements,
+// w FP32 [d] or null, cos / sin FP32 [table, rot / 2] or null, pos int32
+// [batch, tokens] (batch stride pos_sb) or null.  A side with batch, tokens or
+// heads 0 is empty.
+struct QkSideArgs {
+    const uint16_t* x;
+    uint16_t* y;
+    int64_t x_sb, x_st, x_sh, y_sb, y_st, y_sh;
+    int64_t batch, tokens, heads;
+    const float* w;
+    const float* cos;
+    const float* sin;
+    int64_t table;
+    const int32_t* pos;
+    int64_t pos_sb;
+};
+hipError_t launch_qk_norm_rope(const QkSideArgs& q, const QkSideArgs& k, int64_t d, int64_t rot, bool half,
+                               bool fp16, float eps, hipStream_t st);
+
+// Attention over encoder keys and values (attn.hip): q, o [batch, tq, heads,
+// d], k, v [kv_batch, tk, kv_heads, d], strides in elements; kv_len int32
+// [kv_batch] or null, mask bytes [kv_batch, tk] (batch stride mask_sb) or null.
+// Only tk may be 0.
+struct AttnArgs {
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;
+    uint16_t* o;
+    int64_t q_sb, q_st, q_sh, k_sb, k_st, k_sh, v_sb, v_st, v_sh, o_sb, o_st, o_sh;
+    int64_t batch, kv_batch, tq, tk, heads, kv_heads, d;
+    bool fp16;
+    float scale;
+    const int32_t* kv_len;
+    const uint8_t* mask;
+    int64_t mask_sb;
+    void* ws;
+};
+size_t cross_attn_workspace(int64_t batch, int64_t kv_batch, int64_t tq, int64_t tk, int64_t heads,
+                            int64_t kv_heads, int64_t d);
+hipError_t launch_cross_attn(const AttnArgs& a, hipStream_t st);
+
 // Measurement kernels (probe.hip): the INT8 MFMA loop on one workgroup per CU
 // (optionally reading 0.5 KB of LDS per MFMA), and a row stream with a given
 // read / write byte count per row.
