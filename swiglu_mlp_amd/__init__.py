@@ -161,6 +161,13 @@ def _stream(t):
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
+def _raw_stream(dev):
+    """The current stream of device index `dev`, as _stream, without building a
+    Stream object (a microsecond less on calls of a few)."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
 def _need(t, dtype, ndim, what):
     import torch
     if not isinstance(t, torch.Tensor):
@@ -676,28 +683,39 @@ _PAIRING = {"half": CK_PAIR_HALF, "interleaved": CK_PAIR_INTERLEAVED}
 _PACK_HEADS, _PACK_SIDE = struct.Struct("4Q"), struct.Struct("17Q")
 
 
-def _heads(t, what, dtype=None, dev=None):
+def _heads(t, what, dtype, dev):
     """Check a [batch, tokens, heads, d] tensor of 16-bit values; returns the
-    words of its ck_heads (address, batch, token and head strides)."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{what} must be a torch.Tensor")
-    if t.device.type != "cuda" or (dev is not None and t.device != dev):
-        raise ValueError(f"{what} must be on {dev or 'a GPU'}, got {t.device}")
-    if t.dtype not in (torch.bfloat16, torch.float16) or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{what} needs dtype {dtype or 'bfloat16 or float16'}, got {t.dtype}")
-    if t.dim() != 4:
-        raise ValueError(f"{what} needs [batch, tokens, heads, d], got shape {tuple(t.shape)}")
-    sizes, strides = t.shape, t.stride()
-    if sizes[3] < 8 or sizes[3] % 8:
-        raise ValueError(f"{what}: the head size must be a multiple of 8, got {sizes[3]}")
-    if strides[3] != 1:
-        raise ValueError(f"{what}: the channels of a head must be contiguous")
+    words of its ck_heads (address, batch, token and head strides).  dev: the
+    device index the call runs on."""
+    if t.dtype is not dtype or not t.is_cuda or t.get_device() != dev or t.dim() != 4:
+        raise ValueError(f"{what} needs a {dtype} [batch, tokens, heads, d] tensor on cuda:{dev}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    (b, n, h, d), (sb, sn, sh, sd) = t.shape, t.stride()
     # the stride of a dimension of one element is never used
-    words = [t.data_ptr()] + [st if n > 1 else 0 for n, st in zip(sizes[:3], strides)]
-    if words[0] % 16 or any(w % 8 for w in words[1:]):
-        raise ValueError(f"{what} needs 16-byte aligned heads (strides in multiples of 8 elements)")
-    return words
+    if b < 2:
+        sb = 0
+    if n < 2:
+        sn = 0
+    if h < 2:
+        sh = 0
+    p = t.data_ptr()
+    if sd != 1 or d < 8 or d & 7 or p & 15 or (sb | sn | sh) & 7:
+        raise ValueError(f"{what} needs contiguous heads of a multiple of 8 channels, 16-byte aligned (strides in "
+                         f"multiples of 8 elements), got shape {tuple(t.shape)}, strides {t.stride()}")
+    return p, sb, sn, sh
+
+
+def _first(t, what):
+    """The dtype code, dtype and device index that a call takes from its queries."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{what} must be a torch.Tensor on a GPU")
+    dtype = t.dtype
+    if dtype is torch.bfloat16:
+        return CK_DTYPE_BF16, dtype, t.get_device()
+    if dtype is torch.float16:
+        return CK_DTYPE_FP16, dtype, t.get_device()
+    raise ValueError(f"{what} needs dtype bfloat16 or float16, got {dtype}")
 
 
 def _view_span(t):
@@ -723,54 +741,58 @@ def _disjoint(a, b):
     return w[0] <= gap and gap + w[1] <= pitch
 
 
-def _heads_out(out, shape, dtype, dev, what, reads, same=None):
-    """An output of `shape`: a new contiguous tensor, or `out` checked; it may
-    not share elements with `reads`, or else be `same` itself."""
-    import torch
+def _heads_out(out, like, words, what, others, in_place, dtype, dev):
+    """An output shaped like the queries or keys `like` (whose ck_heads words
+    are `words`), and its own words: a new contiguous tensor, or `out` checked.
+    `out` shares no element with `like` and the `others`, or it is `like` itself
+    where `in_place` allows that (each head is read before it is written)."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _heads(out, what, dtype, dev)
-    if tuple(out.shape) != tuple(shape):
-        raise ValueError(f"{what} needs shape {tuple(shape)}, got {tuple(out.shape)}")
-    for n, st in zip(out.shape, out.stride()):
-        if n > 1 and st == 0:
-            raise ValueError(f"{what} must not be an expanded tensor")
-    for t in reads:
-        if t is None or (t is same and t.data_ptr() == out.data_ptr() and t.stride() == out.stride()):
-            continue
-        if not _disjoint(out, t):
-            raise ValueError(f"{what} must not share memory with what the call reads")
-    return out
+        out = like.new_empty(like.shape)
+        _, n, h, d = like.shape
+        return out, (out.data_ptr(), n * h * d, h * d, d)
+    at = _heads(out, what, dtype, dev)
+    if out.shape != like.shape:
+        raise ValueError(f"{what} needs shape {tuple(like.shape)}, got {tuple(out.shape)}")
+    if any(n > 1 and st == 0 for n, st in zip(out.shape, out.stride())):
+        raise ValueError(f"{what} must not be an expanded tensor")
+    if not in_place or at != words:
+        others = (like, *others)
+    if not all(_disjoint(out, t) for t in others):
+        raise ValueError(f"{what} must not share memory with what the call reads")
+    return out, at
 
 
-def _qk_side(x, y, weight, rope, pos, what, d, dev):
-    """The words of one side's ck_qk_side (include/ck.h)."""
+def _qk_side(x, y, weight, rope, pos, d, half, what, dev):
+    """One side's ck_qk_side (include/ck.h), packed; x and y: ck_heads words."""
     import torch
-    b, t, h = x.shape[:3]
-    words = _heads(x, what, None, dev) + _heads(y, what + "_out", x.dtype, dev) + [b, t, h]
+    b, n, h = x[1]
+    w = cos_p = sin_p = rows = pos_p = pos_st = 0
     if weight is not None:
-        _need(weight, torch.float32, 1, what + "_weight")
-        if weight.shape[0] != d or weight.device != dev:
-            raise ValueError(f"{what}_weight needs a ({d},) tensor on {dev}")
-    words.append(weight.data_ptr() if weight is not None else 0)
-    if rope is None:
-        if pos is not None:
-            raise ValueError(f"{what}_pos without {what}_rope")
-        return words + [0, 0, 0, 0, 0]
-    cos, sin = rope
-    for name, tab in (("cos", cos), ("sin", sin)):
-        _need(tab, torch.float32, 2, f"{what}_rope {name}")
-        if tab.shape != cos.shape or tab.device != dev:
-            raise ValueError(f"{what}_rope needs cos and sin of one shape on {dev}")
-    words += [cos.data_ptr(), sin.data_ptr(), cos.shape[0]]
-    if pos is None:
-        if t > cos.shape[0]:
-            raise ValueError(f"{what}_rope has {cos.shape[0]} rows for {t} tokens")
-        return words + [0, 0]
-    if (not isinstance(pos, torch.Tensor) or pos.dtype != torch.int32 or pos.device != dev
-            or tuple(pos.shape) != (b, t) or (t > 1 and pos.stride(1) != 1)):
-        raise ValueError(f"{what}_pos needs an int32 ({b}, {t}) tensor with contiguous rows on {dev}")
-    return words + [pos.data_ptr(), pos.stride(0) if b > 1 else 0]
+        if (weight.dtype is not torch.float32 or weight.shape != (d,) or not weight.is_cuda
+                or weight.get_device() != dev or not weight.is_contiguous()):
+            raise ValueError(f"{what}_weight needs a contiguous float32 ({d},) tensor on cuda:{dev}")
+        w = weight.data_ptr()
+    if rope is not None:
+        cos, sin = rope
+        for t in rope:
+            if (t.dtype is not torch.float32 or t.dim() != 2 or t.shape[1] != half or not t.is_cuda
+                    or t.get_device() != dev or not t.is_contiguous()):
+                raise ValueError(f"{what}_rope needs contiguous float32 [rows, {half}] cos and sin on cuda:{dev}")
+        rows = cos.shape[0]
+        if sin.shape[0] != rows:
+            raise ValueError(f"{what}_rope needs cos and sin of one shape")
+        cos_p, sin_p = cos.data_ptr(), sin.data_ptr()
+        if pos is None:
+            if n > rows:
+                raise ValueError(f"{what}_rope has {rows} rows for {n} tokens")
+        else:
+            if (pos.dtype is not torch.int32 or pos.shape != (b, n) or not pos.is_cuda or pos.get_device() != dev
+                    or (n > 1 and pos.stride(1) != 1)):
+                raise ValueError(f"{what}_pos needs an int32 ({b}, {n}) tensor with contiguous rows on cuda:{dev}")
+            pos_p, pos_st = pos.data_ptr(), pos.stride(0) if b > 1 else 0
+    elif pos is not None:
+        raise ValueError(f"{what}_pos without {what}_rope")
+    return _PACK_SIDE.pack(*x[0], *y, b, n, h, w, cos_p, sin_p, rows, pos_p, pos_st)
 
 
 def ck_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, q_rope=None, k_rope=None, q_pos=None,
@@ -787,39 +809,37 @@ def ck_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, q_rope=None, k_rope
     themselves.  Returns q_out, or (q_out, k_out) when k is given."""
     if pairing not in _PAIRING:
         raise ValueError(f"unknown pairing {pairing!r}")
-    _heads(q, "q")
-    dev, d = q.device, q.shape[3]
-    rot = 0
+    code, dtype, dev = _first(q, "q")
+    hq = _heads(q, "q", dtype, dev)
+    *q_sizes, d = q.shape
+    half = 0
     for rope in (q_rope, k_rope):
-        if rope is None:
-            continue
-        if not isinstance(rope, (tuple, list)) or len(rope) != 2:
-            raise ValueError("a rope is (cos, sin)")
-        r = 2 * rope[0].shape[-1]
-        if rot and r != rot:
-            raise ValueError("q_rope and k_rope turn different numbers of channels")
-        rot = r
-    step = 16 if pairing == "half" else 8
-    if rot > d or rot % step:
-        raise ValueError(f"the rotated channels must be a multiple of {step} up to {d}, got {rot}")
+        if rope is not None:
+            if not isinstance(rope, (tuple, list)) or len(rope) != 2:
+                raise ValueError("a rope is (cos, sin)")
+            if half and rope[0].shape[-1] != half:
+                raise ValueError("q_rope and k_rope turn different numbers of channels")
+            half = rope[0].shape[-1]
+    if 2 * half > d or half % (8 if pairing == "half" else 4):
+        raise ValueError(f"the rotated channels must be a multiple of {16 if pairing == 'half' else 8} up to {d}, "
+                         f"got {2 * half}")
     if d > 256:
         raise ValueError(f"head size {d} is over 256")
-    if k is None and not (k_weight is None and k_rope is None and k_pos is None and k_out is None):
-        raise ValueError("arguments for k without k")
-    y = _heads_out(q_out, q.shape, q.dtype, dev, "q_out", (q, k), q)
-    side_q = _PACK_SIDE.pack(*_qk_side(q, y, q_weight, q_rope, q_pos, "q", d, dev))
-    side_k = z = None
+    y, hy = _heads_out(q_out, q, hq, "q_out", () if k is None else (k,), True, dtype, dev)
+    side_q = _qk_side((hq, q_sizes), hy, q_weight, q_rope, q_pos, d, half, "q", dev)
+    z = side_k = None
     if k is not None:
-        _heads(k, "k", q.dtype, dev)
-        if k.shape[3] != d:
-            raise ValueError(f"q and k need one head size, got {d} and {k.shape[3]}")
-        z = _heads_out(k_out, k.shape, q.dtype, dev, "k_out", (q, k), k)
+        hk = _heads(k, "k", dtype, dev)
+        *k_sizes, dk = k.shape
+        if dk != d:
+            raise ValueError(f"q and k need one head size, got {d} and {dk}")
+        z, hz = _heads_out(k_out, k, hk, "k_out", (q,), True, dtype, dev)
         if q_out is not None and k_out is not None and not _disjoint(y, z):
             raise ValueError("q_out and k_out must not share memory")
-        side_k = _PACK_SIDE.pack(*_qk_side(k, z, k_weight, k_rope, k_pos, "k", d, dev))
-    import torch
-    _call("ck_qk_norm_rope", side_q, side_k, d, rot, _PAIRING[pairing],
-          CK_DTYPE_FP16 if q.dtype == torch.float16 else CK_DTYPE_BF16, eps, _stream(q))
+        side_k = _qk_side((hk, k_sizes), hz, k_weight, k_rope, k_pos, d, half, "k", dev)
+    elif k_weight is not None or k_rope is not None or k_pos is not None or k_out is not None:
+        raise ValueError("arguments for k without k")
+    _call("ck_qk_norm_rope", side_q, side_k, d, 2 * half, _PAIRING[pairing], code, eps, _raw_stream(dev))
     return y if k is None else (y, z)
 
 
@@ -834,11 +854,11 @@ def ck_cross_attn(q, k, v, scale=None, kv_len=None, key_mask=None, out=None, wor
     left out is not read; a row with no key is zero.
     Returns [batch, tq, heads, d], contiguous unless `out` is given."""
     import torch
-    hq = _heads(q, "q")
-    dev, (b, tq, h, d) = q.device, q.shape
-    hk, hv = _heads(k, "k", q.dtype, dev), _heads(v, "v", q.dtype, dev)
+    code, dtype, dev = _first(q, "q")
+    hq, hk, hv = _heads(q, "q", dtype, dev), _heads(k, "k", dtype, dev), _heads(v, "v", dtype, dev)
+    b, tq, h, d = q.shape
     kb, tk, kh, dk = k.shape
-    if tuple(v.shape) != (kb, tk, kh, dk):
+    if v.shape != k.shape:
         raise ValueError(f"k and v need one shape, got {tuple(k.shape)} and {tuple(v.shape)}")
     if dk != d or d > 128:
         raise ValueError(f"q and k need one head size up to 128, got {d} and {dk}")
@@ -847,24 +867,26 @@ def ck_cross_attn(q, k, v, scale=None, kv_len=None, key_mask=None, out=None, wor
     scale = d ** -0.5 if scale is None else float(scale)
     if not 0.0 < scale < 3.4e38:
         raise ValueError(f"scale must be positive and finite, got {scale}")
+    len_p = mask_p = ws_p = None
+    mask_st = ws_n = 0
     if kv_len is not None:
-        _need(kv_len, torch.int32, 1, "kv_len")
-        if kv_len.shape[0] != kb or kv_len.device != dev:
-            raise ValueError(f"kv_len needs ({kb},) on {dev}")
-    stride = 0
+        if (kv_len.dtype is not torch.int32 or kv_len.shape != (kb,) or not kv_len.is_cuda
+                or kv_len.get_device() != dev or not kv_len.is_contiguous()):
+            raise ValueError(f"kv_len needs a contiguous int32 ({kb},) tensor on cuda:{dev}")
+        len_p = kv_len.data_ptr()
     if key_mask is not None:
-        if (not isinstance(key_mask, torch.Tensor) or key_mask.dtype not in (torch.bool, torch.uint8)
-                or key_mask.device != dev or tuple(key_mask.shape) != (kb, tk)
-                or (tk > 1 and key_mask.stride(1) != 1)):
-            raise ValueError(f"key_mask needs a bool or uint8 ({kb}, {tk}) tensor with contiguous rows on {dev}")
-        stride = key_mask.stride(0) if kb > 1 else 0
-    y = _heads_out(out, q.shape, q.dtype, dev, "out", (q, k, v))
+        if (key_mask.dtype not in (torch.bool, torch.uint8) or key_mask.shape != (kb, tk) or not key_mask.is_cuda
+                or key_mask.get_device() != dev or (tk > 1 and key_mask.stride(1) != 1)):
+            raise ValueError(f"key_mask needs a bool or uint8 ({kb}, {tk}) tensor with contiguous rows on cuda:{dev}")
+        mask_p, mask_st = key_mask.data_ptr(), key_mask.stride(0) if kb > 1 else 0
+    y, hy = _heads_out(out, q, hq, "out", (k, v), False, dtype, dev)
     need = lib().ck_cross_attn_workspace_size(b, kb, tq, tk, h, kh, d)
-    ws = _workspace(workspace, need, dev) if need else None
+    if need:
+        ws = _workspace(workspace, need, q.device)
+        ws_p, ws_n = ws.data_ptr(), ws.numel()
     pack = _PACK_HEADS.pack
-    _call("ck_cross_attn", pack(*hq), pack(*hk), pack(*hv), pack(*_heads(y, "out")), b, kb, tq, tk, h, kh, d,
-          CK_DTYPE_FP16 if q.dtype == torch.float16 else CK_DTYPE_BF16, scale, _ptr(kv_len), _ptr(key_mask),
-          stride, _ptr(ws), ws.numel() if need else 0, _stream(q))
+    _call("ck_cross_attn", pack(*hq), pack(*hk), pack(*hv), pack(*hy), b, kb, tq, tk, h, kh, d, code, scale,
+          len_p, mask_p, mask_st, ws_p, ws_n, _raw_stream(dev))
     return y
 
 

@@ -26,11 +26,22 @@
 // 16-byte chunks of a row are permuted on the source side (k_swz, v_swz) such
 // that the reads of both operands touch every LDS bank once.
 //
-// Keys that are not allowed are never read: their lanes load from past the
-// buffer, which gives zeros, so infinities and NaN there cannot reach a
-// product, and their scores are set to -inf.
+// Keys that are not allowed are never read.  With a key mask the workgroup
+// lists the allowed keys of the next 4096 in LDS (their order kept) and the
+// tiles are made of those, so a dropped key costs neither its bytes nor its
+// products; lanes past the last key load from past the buffer, which gives
+// zeros, and their scores are set to -inf.
+//
+// Two kernels.  tile_kernel: the waves of a workgroup hold different rows and
+// share each K / V tile (many rows: bound by the matrix cores).  slice_kernel:
+// the waves hold the same 32 rows and each streams its own 32-key slices
+// through LDS of its own, without a barrier (few rows: bound by HBM).  Either
+// may split the keys over several workgroups; the unnormalised FP32 partial
+// results then go to the workspace and join_kernel adds them in a fixed order.
 #include "ck_internal.hpp"
 #include "heads.hpp"
+
+#include <algorithm>
 
 namespace ck {
 namespace attn {
@@ -43,7 +54,7 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
-constexpr int kTile = 64;   // keys per tile
+constexpr int kList = 4096;   // keys whose mask is listed at a time
 
 struct Params {
     const uint16_t* q;
@@ -55,13 +66,23 @@ struct Params {
     const uint8_t* mask;
     int64_t mask_sb;
     uint32_t tk, d, share, heads_kv, rows, m_tiles;
+    uint32_t splits, split_keys;    // keys [split_keys s, split_keys (s + 1)) belong to split s
+    uint32_t list_keys;             // keys listed at a time: at most kList, their offsets in 32 bits
     float c;                        // scale * log2(e)
-    FastDiv by_g, by_tq, by_hkv, by_tiles;
+    float* part_o;                  // [key head, row][split][d]
+    float* part_ml;                 // [key head, row][split] (m, l)
+    FastDiv by_g, by_tq, by_hkv, by_tiles, by_splits;
 };
 
 #if defined(__HIP_DEVICE_COMPILE__)
 
-__device__ __forceinline__ void wait_vm0() { __builtin_amdgcn_s_waitcnt(0x0F70); }   // vmcnt(0) only
+// s_waitcnt vmcnt(N) alone
+template <int N>
+__device__ __forceinline__ void wait_vmcnt()
+{
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
 
 // s_barrier without a fence; the empty asm statements keep memory accesses on
 // their side of it.
@@ -74,7 +95,7 @@ __device__ __forceinline__ void workgroup_barrier()
 
 // 16 bytes per lane from a buffer to LDS: lane l's land at byte lds + 16 l.
 // Inline assembly, so that the compiler does not wait for it before unrelated
-// LDS reads; the caller waits (wait_vm0) before the data's first use.
+// LDS reads; the caller waits (wait_vmcnt) before the data's first use.
 __device__ __forceinline__ void lds_dma_b128(v4i rsrc, uint32_t voff, uint32_t lds)
 {
     asm volatile(
@@ -134,170 +155,199 @@ __device__ __forceinline__ float half_sum(float x)
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-#endif
+// What one lane knows of its row and its workgroup's keys.
+struct Place {
+    uint32_t half, col;        // lane / 32, lane % 32
+    uint32_t bh, hk, eb;       // key head of the call, of its sequence; encoder sequence
+    uint32_t split, row;       // row: of the key head's list, may be past the last
+    uint32_t first, last;      // this workgroup's keys
+    int64_t q_at, o_at;        // element offsets of the row
+};
 
-// DP: channels padded to 64, 96 or 128 (the chunks past d load zeros).
-// NW: waves per workgroup, 32 rows each.
-template <typename T, int DP, int NW>
-__global__ __launch_bounds__(NW * 64, 2) void tile_kernel(Params p)
+// Workgroup index -> (key head, row tile, split); rows tiles of 32 `waves`.
+__device__ __forceinline__ Place place_of(const Params& p, uint32_t block, uint32_t row_in_tile, uint32_t tile_rows)
 {
-#if defined(__HIP_DEVICE_COMPILE__)
-    constexpr int CH = DP / 8;                       // 16-byte chunks per row
-    constexpr int TILE_B = kTile * DP * 2;           // bytes of one K or V tile
-    constexpr int NI = TILE_B / 1024;                // loads (1 KB) per K or V tile
-    constexpr int PER = 2 * NI / NW;                 // ... of the pair, per wave
-    static_assert(2 * NI % NW == 0, "loads split evenly over the waves");
-    constexpr int KS = DP / 16;                      // 16-channel steps of S
-    constexpr int DB = DP / 32;                      // 32-channel blocks of O
-    // FP16 probabilities are scaled by 2^6, so small ones keep their bits: with
-    // the deferred maximum below they reach at most 2^14.
-    constexpr float kLift = __is_same(T, f16) ? 6.0f : 0.0f;
-    constexpr float kDefer = 8.0f;
-    __shared__ __attribute__((aligned(1024))) char smem[2 * 2 * TILE_B];
-
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const uint32_t half = lane >> 5, col = lane & 31;
-
-    // workgroup -> (encoder sequence, key head, row tile)
-    const uint32_t bh = p.by_tiles.div(blockIdx.x);
-    const uint32_t mt = blockIdx.x - bh * p.m_tiles;
-    const uint32_t eb = p.by_hkv.div(bh);
-    const uint32_t hk = bh - eb * p.heads_kv;
-
-    // this lane's row -> (sequence, token, head)
-    const uint32_t row = (mt * NW + wave) * 32 + col;
-    const uint32_t rr = row < p.rows ? row : p.rows - 1;
-    const uint32_t rt = p.by_g.div(rr);
-    const uint32_t head = hk * p.by_g.d + (rr - rt * p.by_g.d);
+    Place w;
+    const uint32_t lane = threadIdx.x & 63;
+    w.half = lane >> 5, w.col = lane & 31;
+    const uint32_t rest = p.by_splits.div(block);
+    w.split = block - rest * p.splits;
+    w.bh = p.by_tiles.div(rest);
+    w.eb = p.by_hkv.div(w.bh);
+    w.hk = w.bh - w.eb * p.heads_kv;
+    w.row = (rest - w.bh * p.m_tiles) * tile_rows + row_in_tile + w.col;
+    const uint32_t r = w.row < p.rows ? w.row : p.rows - 1;   // rows past the last compute the last, and store nothing
+    const uint32_t rt = p.by_g.div(r);
+    const uint32_t head = w.hk * p.by_g.d + (r - rt * p.by_g.d);
     const uint32_t si = p.by_tq.div(rt);
     const uint32_t tok = rt - si * p.by_tq.d;
-    const int64_t seq = (int64_t)eb * p.share + si;
-
-    v4u q[KS];
-    {
-        const uint16_t* qp = p.q + seq * p.q_sb + (int64_t)tok * p.q_st + (int64_t)head * p.q_sh;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            const uint32_t c = 16 * s + 8 * half;
-            q[s] = v4u{0, 0, 0, 0};
-            if (c < p.d) q[s] = *reinterpret_cast<const v4u*>(qp + c);
-        }
-    }
-
+    const int64_t seq = (int64_t)w.eb * p.share + si;
+    w.q_at = seq * p.q_sb + (int64_t)tok * p.q_st + (int64_t)head * p.q_sh;
+    w.o_at = seq * p.o_sb + (int64_t)tok * p.o_st + (int64_t)head * p.o_sh;
     uint32_t len = p.tk;
     if (p.kv_len) {
-        const int32_t l = p.kv_len[eb];
+        const int32_t l = p.kv_len[w.eb];
         len = l < 0 ? 0u : min((uint32_t)l, p.tk);
     }
-    const uint32_t tiles = (len + kTile - 1) / kTile;
-    const uint8_t* mask = p.mask ? p.mask + (int64_t)eb * p.mask_sb : nullptr;
+    w.first = min(w.split * p.split_keys, len);
+    w.last = min(w.first + p.split_keys, len);
+    return w;
+}
 
-    // this wave's loads: load j of the 2 NI (K's, then V's) fills bytes 1024 j .. of a buffer
-    const char* k_base = reinterpret_cast<const char*>(p.k + (int64_t)eb * p.k_sb + (int64_t)hk * p.k_sh);
-    const char* v_base = reinterpret_cast<const char*>(p.v + (int64_t)eb * p.v_sb + (int64_t)hk * p.v_sh);
-    const uint32_t k_pitch = (uint32_t)(p.k_st * 2), v_pitch = (uint32_t)(p.v_st * 2);
-    uint32_t src_row[PER], src_off[PER];
+template <int DP>
+__device__ __forceinline__ void load_q(const Params& p, const Place& w, v4u (&q)[DP / 16])
+{
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int j = wave * PER + i;
-        const bool is_v = j >= NI;
-        const uint32_t slot = (uint32_t)(is_v ? j - NI : j) * 64 + lane;
-        const uint32_t r = slot / CH, place = slot % CH;
-        const uint32_t c = is_v ? v_swz<CH>(r, place) : k_swz<CH>(r, place);   // both are involutions
-        src_row[i] = r;
-        src_off[i] = 8 * c < p.d ? r * (is_v ? v_pitch : k_pitch) + 16 * c : kBufferOutside;
+    for (int s = 0; s < DP / 16; ++s) {
+        const uint32_t c = 16 * s + 8 * w.half;
+        q[s] = v4u{0, 0, 0, 0};
+        if (c < p.d) q[s] = *reinterpret_cast<const v4u*>(p.q + w.q_at + c);
     }
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
+}
 
-    auto tile_bits = [&](uint32_t t, uint32_t mbyte) -> uint64_t {   // allowed keys of tile t
-        const uint32_t left = len - t * kTile;
-        uint64_t bits = left >= 64 ? ~0ull : (1ull << left) - 1;
-        if (mask) bits &= __ballot(mbyte != 0);
-        return bits;
-    };
-    auto mask_byte = [&](uint32_t t) -> uint32_t {
-        const uint32_t j = t * kTile + lane;
-        return mask && j < len ? mask[j] : 0u;
-    };
-    auto load_tile = [&](uint32_t t, uint64_t bits) {
-        const v4i rk = make_rsrc(k_base + (uint64_t)t * kTile * k_pitch);
-        const v4i rv = make_rsrc(v_base + (uint64_t)t * kTile * v_pitch);
+// The indices (from `from`) of the allowed keys among [from, from + n), n <=
+// kList, in order; returns their number.  All NT threads of the workgroup
+// call it together; counts: one word per wave of LDS.
+template <int NT>
+__device__ uint32_t list_keys(const uint8_t* mask, uint32_t from, uint32_t n, uint16_t* list, uint32_t* counts)
+{
+    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    uint32_t total = 0;
+    for (uint32_t r = 0; r < n; r += NT * 8) {
+        const uint32_t j = r + tid * 8;
+        uint32_t keep = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (j + e < n && mask[(uint64_t)from + j + e]) keep |= 1u << e;
+        const uint32_t mine = __popc(keep);
+        uint32_t upto = mine;   // inclusive count over the wave
+#pragma unroll
+        for (int s = 1; s < 64; s <<= 1) {
+            const uint32_t x = __shfl_up(upto, s);
+            if (lane >= (uint32_t)s) upto += x;
+        }
+        __syncthreads();   // counts of the round before are read
+        if (lane == 63) counts[wave] = upto;
+        __syncthreads();
+        uint32_t at = total + upto - mine;
+#pragma unroll
+        for (int w = 0; w < NT / 64; ++w) {
+            const uint32_t c = counts[w];
+            if ((uint32_t)w < wave) at += c;
+            total += c;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (keep >> e & 1) list[at++] = (uint16_t)(j + e);
+    }
+    __syncthreads();
+    return total;
+}
+
+// A wave's loads of 16-byte chunks from rows of K and V into LDS: rows of NK
+// keys of K, then of V; this wave issues loads first .. first + PER - 1.
+// LISTED: the keys come through a list of their indices.
+template <int DP, int NK, int PER, bool LISTED>
+struct Loader {
+    static constexpr int CH = DP / 8, NI = NK * DP * 2 / 1024;
+    const char *k, *v;           // of key 0 of the head
+    uint32_t k_pitch, v_pitch, d, lane;
+    uint32_t off[PER];           // of this lane's chunk: in its row (LISTED) or in the tile
+
+    __device__ __forceinline__ uint32_t row(int j) const { return ((j < NI ? j : j - NI) * 64 + lane) / CH; }
+    __device__ __forceinline__ uint32_t chunk(int j) const
+    {
+        const uint32_t r = row(j), at = ((j < NI ? j : j - NI) * 64 + lane) % CH;
+        const uint32_t c = j < NI ? k_swz<CH>(r, at) : v_swz<CH>(r, at);   // both are their own inverse
+        return 8 * c < d ? 16 * c : kBufferOutside;
+    }
+    __device__ __forceinline__ void init(const Params& p, const Place& w, int first)
+    {
+        lane = threadIdx.x & 63;
+        d = p.d;
+        k = reinterpret_cast<const char*>(p.k + (int64_t)w.eb * p.k_sb + (int64_t)w.hk * p.k_sh);
+        v = reinterpret_cast<const char*>(p.v + (int64_t)w.eb * p.v_sb + (int64_t)w.hk * p.v_sh);
+        k_pitch = (uint32_t)(p.k_st * 2), v_pitch = (uint32_t)(p.v_st * 2);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int j = wave * PER + i;
-            uint32_t off = src_off[i];
-            if (bits != ~0ull && !((bits >> src_row[i]) & 1)) off = kBufferOutside;
-            lds_dma_b128(j >= NI ? rv : rk, off, lds0 + (t & 1) * 2 * TILE_B + j * 1024);
+            off[i] = chunk(first + i);   // past d: 2^31, and past the buffer with any row's offset added
+            if constexpr (!LISTED) off[i] += row(first + i) * (first + i < NI ? k_pitch : v_pitch);
         }
-    };
+    }
+    // keys key .. key + NK - 1, or key + list[0 .. NK - 1]; only the first
+    // `left` are there
+    __device__ __forceinline__ void load(uint32_t key, const uint16_t* list, uint32_t left, int first,
+                                         uint32_t lds) const
+    {
+        const v4i rk = make_rsrc(k + (uint64_t)key * k_pitch), rv = make_rsrc(v + (uint64_t)key * v_pitch);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int j = first + i;
+            uint32_t at = off[i];
+            if constexpr (LISTED) at += list[min(row(j), left - 1)] * (j < NI ? k_pitch : v_pitch);
+            if (left < (uint32_t)NK && row(j) >= left) at = kBufferOutside;
+            lds_dma_b128(j < NI ? rk : rv, at, lds + j * 1024);
+        }
+    }
+};
 
+// The running softmax of one row (m: of the raw scores) and its accumulators.
+// FP16 probabilities are scaled by 2^kLift, so that small ones keep their bits:
+// with the deferred maximum below they reach at most 2^14.
+template <typename T, int DP>
+struct Row {
+    static constexpr int CH = DP / 8, DB = DP / 32, KS = DP / 16;
+    static constexpr float kLift = __is_same(T, f16) ? 6.0f : 0.0f;
+    static constexpr float kDefer = 8.0f;
     v16f o[DB];
-#pragma unroll
-    for (int b = 0; b < DB; ++b)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[b][i] = 0.0f;
-    float m = -__builtin_inff(), l = 0.0f;
-    bool any = false;   // whether any key was allowed (the same for all rows)
+    float m, l;
 
-    uint64_t bits = 0;
-    uint32_t next_byte = 0;
-    if (tiles) {
-        bits = tile_bits(0, mask_byte(0));
-        load_tile(0, bits);
-        next_byte = mask_byte(1);
+    __device__ __forceinline__ void clear()
+    {
+        m = -__builtin_inff();
+        l = 0.0f;
+#pragma unroll
+        for (int b = 0; b < DB; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[b][i] = 0.0f;
     }
 
-    const uint32_t k_row = col * CH;                       // K fragment: row col (+ 32), chunk 2 s + half
-    const uint32_t g16 = lane >> 4, j16 = lane & 15;       // V fragment: see the transposing read above
-    const uint32_t v_key = 4 * (g16 >> 1) + (j16 >> 2);
-    const uint32_t v_chunk = 2 * (g16 & 1) + ((j16 & 3) >> 1);
-
-    for (uint32_t t = 0; t < tiles; ++t) {
-        wait_vm0();
-        workgroup_barrier();   // tile t is in LDS, and every wave is done with the other buffer
-        uint64_t next_bits = 0;
-        if (t + 1 < tiles) {
-            next_bits = tile_bits(t + 1, next_byte);
-            load_tile(t + 1, next_bits);
-            if (t + 2 < tiles) next_byte = mask_byte(t + 2);
-        }
-        const char* kb = smem + (t & 1) * 2 * TILE_B;
-        const char* vb = kb + TILE_B;
-
-        v16f s[2];
+    // 32 N keys in LDS (K rows at kb, V rows at vb), the first `left` of them
+    // real.
+    template <int N>
+    __device__ __forceinline__ void step(const char* kb, const char* vb, const v4u (&q)[KS], uint32_t left, float c,
+                                         uint32_t half, uint32_t col)
+    {
+        v16f s[N];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+        for (int n = 0; n < N; ++n) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[n][i] = 0.0f;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                const uint32_t at = (k_row + n * 32 * CH + k_swz<CH>(col, 2 * ks + half)) * 16;
+                const uint32_t at = ((col + n * 32) * CH + k_swz<CH>(col, 2 * ks + half)) * 16;
                 s[n] = mfma<T>(*reinterpret_cast<const v4u*>(kb + at), q[ks], s[n]);
             }
         }
-        any |= bits != 0;
-        if (bits != ~0ull) {
+        if (left < 32u * N) {
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const uint32_t w = (uint32_t)(bits >> (32 * n)) >> (4 * half);
+            for (int n = 0; n < N; ++n)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    if (!((w >> ((i & 3) + 8 * (i >> 2))) & 1u)) s[n][i] = -__builtin_inff();
-            }
+                    if (n * 32 + (i & 3) + 8 * (i >> 2) + 4 * half >= left) s[n][i] = -__builtin_inff();
         }
+        float mx = s[0][0];
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[n][i]);
+        mx = half_max(mx);
         // The maximum in use may lag behind the true one by up to 2^kDefer in
         // the probabilities: FP32 sums and 16-bit floats lose nothing by it, and
         // most tiles skip the rescale of the accumulators.
-        float mx = s[0][0];
-#pragma unroll
-        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[0][i]);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[1][i]);
-        mx = half_max(mx);
-        if (__any((mx - m) * p.c > kDefer)) {
+        if (__any((mx - m) * c > kDefer)) {
             const float mn = fmaxf(m, mx);
-            const float alpha = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f((m - mn) * p.c);
+            const float alpha = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f((m - mn) * c);
             m = mn;
             l = l * alpha;
 #pragma unroll
@@ -305,13 +355,13 @@ __global__ __launch_bounds__(NW * 64, 2) void tile_kernel(Params p)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[b][i] *= alpha;
         }
-        const float shift = (m == -__builtin_inff() ? 0.0f : -m * p.c) + kLift;
-        v4u pf[4];
+        const float shift = (m == -__builtin_inff() ? 0.0f : -m * c) + kLift;
+        v4u pf[2 * N];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+        for (int n = 0; n < N; ++n) {
             float e[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][i], p.c, shift));
+            for (int i = 0; i < 16; ++i) e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][i], c, shift));
             float sum[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) sum[i] = (e[i] + e[i + 4]) + (e[i + 8] + e[i + 12]);
@@ -321,8 +371,10 @@ __global__ __launch_bounds__(NW * 64, 2) void tile_kernel(Params p)
                 pf[2 * n + g] = v4u{pack2<T>(e[8 * g], e[8 * g + 1]), pack2<T>(e[8 * g + 2], e[8 * g + 3]),
                                     pack2<T>(e[8 * g + 4], e[8 * g + 5]), pack2<T>(e[8 * g + 6], e[8 * g + 7])};
         }
+        const uint32_t lane = half * 32 + col, j16 = lane & 15;
+        const uint32_t v_key = 4 * half + (j16 >> 2), v_chunk = 2 * ((lane >> 4) & 1) + ((j16 & 3) >> 1);
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < 2 * N; ++g) {
 #pragma unroll
             for (int b = 0; b < DB; ++b) {
                 typedef __attribute__((address_space(3))) v4s lds_v4s;
@@ -333,57 +385,330 @@ __global__ __launch_bounds__(NW * 64, 2) void tile_kernel(Params p)
                 o[b] = mfma<T>(__builtin_bit_cast(v4u, a), pf[g], o[b]);
             }
         }
-        bits = next_bits;
     }
 
+    // After the last step: the row's whole sum, and the marks of a row without
+    // finite scores: m = -inf where there was no key at all (o = 0), the lowest
+    // float where there were keys and all their scores were -inf (0 / 0).
+    __device__ __forceinline__ void finish(bool any)
+    {
+        l = half_sum(l);
+        if (any && m == -__builtin_inff()) m = -3.402823466e38f;
+    }
+};
+
+#endif
+
+// DP: channels padded to 64, 96 or 128 (the chunks past d load zeros).
+// NW: waves per workgroup, 32 rows each.  Tiles of 64 keys.  MASK: with a key
+// mask (its lists would cost the other calls registers).
+template <typename T, int DP, int NW, bool MASK>
+__global__ __launch_bounds__(NW * 64, 2) void tile_kernel(Params p)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    constexpr int NK = 64, DB = DP / 32;
+    constexpr int TILE_B = NK * DP * 2;              // bytes of one K or V tile
+    constexpr int PER = 2 * TILE_B / 1024 / NW;      // loads (1 KB) of a tile pair per wave
+    static_assert(2 * TILE_B % (1024 * NW) == 0, "loads split evenly over the waves");
+    __shared__ __attribute__((aligned(1024))) char smem[2 * 2 * TILE_B];
+    __shared__ uint16_t list[MASK ? kList : 1];
+    __shared__ uint32_t counts[NW];
+
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Place w = place_of(p, blockIdx.x, wave * 32, NW * 32);
+    v4u q[DP / 16];
+    load_q<DP>(p, w, q);
+    Loader<DP, NK, PER, MASK> ld;
+    ld.init(p, w, wave * PER);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
+    const uint8_t* mask = MASK ? p.mask + (int64_t)w.eb * p.mask_sb : nullptr;
+
+    Row<T, DP> r;
+    r.clear();
+    bool any = false;   // whether any key was allowed (the same for all rows)
+    // without a mask one pass over all keys; with one, a pass for each list
+    for (uint32_t from = w.first; from < w.last;) {
+        uint32_t n = w.last - from;
+        const uint32_t upto = MASK ? from + min(n, p.list_keys) : w.last;
+        if constexpr (MASK) n = list_keys<NW * 64>(mask, from, upto - from, list, counts);
+        any |= n != 0;
+        const uint32_t tiles = (n + NK - 1) / NK;
+        auto load = [&](uint32_t t) {
+            const uint32_t lds = lds0 + (t & 1) * 2 * TILE_B;
+            ld.load(MASK ? from : from + t * NK, list + t * NK, n - t * NK, wave * PER, lds);
+        };
+        if (tiles) load(0);
+        for (uint32_t t = 0; t < tiles; ++t) {
+            wait_vmcnt<0>();
+            workgroup_barrier();   // tile t is in LDS, and every wave is done with the other buffer
+            if (t + 1 < tiles) load(t + 1);
+            const char* kb = smem + (t & 1) * 2 * TILE_B;
+            r.template step<2>(kb, kb + TILE_B, q, n - t * NK, p.c, w.half, w.col);
+        }
+        if constexpr (MASK) workgroup_barrier();   // the list and the buffers are free
+        from = upto;
+    }
+    r.finish(any);
+    if (w.row >= p.rows) return;
+    if (p.splits > 1) {
+        const uint64_t at = ((uint64_t)w.bh * p.rows + w.row) * p.splits + w.split;
+        if (w.half == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(r.m, r.l);
+        float* po = p.part_o + at * p.d + 4 * w.half;
+#pragma unroll
+        for (int b = 0; b < DB; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+                if (32 * b + 2 * i + 4 * w.half < p.d)
+                    *reinterpret_cast<float4*>(po + 32 * b + 2 * i) =
+                        make_float4(r.o[b][i], r.o[b][i + 1], r.o[b][i + 2], r.o[b][i + 3]);
+        return;
+    }
     // o[b][i] is channel 32 b + (i % 4) + 8 (i / 4) + 4 half of row col: pairs
     // of 4-channel groups are exchanged between the halves for 16-byte stores.
-    const float total = half_sum(l);
-    const float inv = any ? 1.0f / total : 0.0f;   // no allowed key: o is zero
-    if (row < p.rows) {
-        uint16_t* op = p.o + seq * p.o_sb + (int64_t)tok * p.o_st + (int64_t)head * p.o_sh;
+    const float inv = r.m == -__builtin_inff() ? 0.0f : 1.0f / r.l;   // no allowed key: o is zero
+    uint16_t* op = p.o + w.o_at;
 #pragma unroll
-        for (int b = 0; b < DB; ++b) {
+    for (int b = 0; b < DB; ++b) {
 #pragma unroll
-            for (int i = 0; i < 16; i += 8) {
-                const uint32_t x0 = pack2<T>(o[b][i] * inv, o[b][i + 1] * inv);
-                const uint32_t x1 = pack2<T>(o[b][i + 2] * inv, o[b][i + 3] * inv);
-                const uint32_t y0 = pack2<T>(o[b][i + 4] * inv, o[b][i + 5] * inv);
-                const uint32_t y1 = pack2<T>(o[b][i + 6] * inv, o[b][i + 7] * inv);
-                const auto r0 = __builtin_amdgcn_permlane32_swap(x0, y0, false, false);
-                const auto r1 = __builtin_amdgcn_permlane32_swap(x1, y1, false, false);
-                const uint32_t c = 32 * b + 2 * i + 8 * half;
-                if (c < p.d) *reinterpret_cast<v4u*>(op + c) = v4u{r0[0], r1[0], r0[1], r1[1]};
-            }
+        for (int i = 0; i < 16; i += 8) {
+            const uint32_t x0 = pack2<T>(r.o[b][i] * inv, r.o[b][i + 1] * inv);
+            const uint32_t x1 = pack2<T>(r.o[b][i + 2] * inv, r.o[b][i + 3] * inv);
+            const uint32_t y0 = pack2<T>(r.o[b][i + 4] * inv, r.o[b][i + 5] * inv);
+            const uint32_t y1 = pack2<T>(r.o[b][i + 6] * inv, r.o[b][i + 7] * inv);
+            const auto r0 = __builtin_amdgcn_permlane32_swap(x0, y0, false, false);
+            const auto r1 = __builtin_amdgcn_permlane32_swap(x1, y1, false, false);
+            const uint32_t c = 32 * b + 2 * i + 8 * w.half;
+            if (c < p.d) *reinterpret_cast<v4u*>(op + c) = v4u{r0[0], r1[0], r0[1], r1[1]};
         }
     }
 #endif
+}
+
+// Few rows: 4 waves on the same 32 rows, each streaming every fourth slice of
+// 32 keys through two buffers of its own.
+template <typename T, int DP, bool MASK>
+__global__ __launch_bounds__(256, 1) void slice_kernel(Params p)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    constexpr int NW = 4, NK = 32, DB = DP / 32;
+    constexpr int SLICE_B = NK * DP * 2;             // bytes of one K or V slice
+    constexpr int PER = 2 * SLICE_B / 1024;          // loads (1 KB) per slice pair
+    constexpr int PITCH = DP + 4;                    // floats per row of the joined accumulators
+    constexpr int RING_B = NW * 2 * 2 * SLICE_B;
+    static_assert(RING_B >= NW * 32 * PITCH * 4, "the accumulators of all waves fit the ring");
+    __shared__ __attribute__((aligned(1024))) char smem[RING_B];
+    __shared__ uint16_t list[MASK ? kList : 1];
+    __shared__ uint32_t counts[NW];
+    __shared__ float2 ml[NW][32];
+
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Place w = place_of(p, blockIdx.x, 0, 32);
+    v4u q[DP / 16];
+    load_q<DP>(p, w, q);
+    Loader<DP, NK, PER, MASK> ld;
+    ld.init(p, w, 0);
+    const char* mine = smem + wave * (2 * 2 * SLICE_B);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem + wave * (2 * 2 * SLICE_B);
+    const uint8_t* mask = MASK ? p.mask + (int64_t)w.eb * p.mask_sb : nullptr;
+
+    Row<T, DP> r;
+    r.clear();
+    bool any = false;
+    for (uint32_t from = w.first; from < w.last;) {
+        uint32_t n = w.last - from;
+        const uint32_t upto = MASK ? from + min(n, p.list_keys) : w.last;
+        if constexpr (MASK) n = list_keys<NW * 64>(mask, from, upto - from, list, counts);
+        any |= n != 0;
+        const uint32_t slices = (n + NK - 1) / NK;
+        auto load = [&](uint32_t t) {
+            const uint32_t lds = lds0 + (t / NW & 1) * 2 * SLICE_B;
+            ld.load(MASK ? from : from + t * NK, list + t * NK, n - t * NK, 0, lds);
+        };
+        if (wave < slices) load(wave);
+        for (uint32_t t = wave; t < slices; t += NW) {
+            if (t + NW < slices) {
+                load(t + NW);
+                wait_vmcnt<PER>();   // all but the loads just issued: slice t is in LDS
+            } else {
+                wait_vmcnt<0>();
+            }
+            asm volatile("" ::: "memory");
+            const char* kb = mine + (t / NW & 1) * 2 * SLICE_B;
+            r.template step<1>(kb, kb + SLICE_B, q, n - t * NK, p.c, w.half, w.col);
+            asm volatile("" ::: "memory");   // its LDS reads end before the next load into this buffer
+        }
+        if constexpr (MASK) __syncthreads();   // the list is free
+        from = upto;
+    }
+    r.finish(any);
+    __syncthreads();       // every wave is done with the ring
+
+    float* acc = reinterpret_cast<float*>(smem);
+    if (w.half == 0) ml[wave][w.col] = make_float2(r.m, r.l);
+    if (w.row < p.rows) {
+        float* a = acc + (wave * 32 + w.col) * PITCH + 4 * w.half;
+#pragma unroll
+        for (int b = 0; b < DB; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<float4*>(a + 32 * b + 2 * i) =
+                    make_float4(r.o[b][i], r.o[b][i + 1], r.o[b][i + 2], r.o[b][i + 3]);
+    }
+    __syncthreads();
+
+    // joined: 8 channels of a row a thread
+    constexpr int CH = DP / 8;
+    const uint32_t row0 = w.row - w.col;   // the tile's first row
+    for (uint32_t e = threadIdx.x; e < 32 * CH; e += 256) {
+        const uint32_t row = e / CH, c = e % CH * 8;
+        if (row0 + row >= p.rows || c >= p.d) continue;
+        float m = ml[0][row].x;
+#pragma unroll
+        for (int i = 1; i < NW; ++i) m = fmaxf(m, ml[i][row].x);
+        float l = 0.0f, x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+            const float2 t = ml[i][row];
+            // (-inf) - (-inf) is no weight: such a wave holds nothing
+            const float f = t.x == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f((t.x - m) * p.c);
+            const float* a = acc + (i * 32 + row) * PITCH + c;
+            l = __builtin_fmaf(t.y, f, l);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) x[u] = __builtin_fmaf(a[u], f, x[u]);
+        }
+        if (p.splits > 1) {
+            const uint64_t at = ((uint64_t)w.bh * p.rows + row0 + row) * p.splits + w.split;
+            if (c == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m, l);
+            float* po = p.part_o + at * p.d + c;
+            *reinterpret_cast<float4*>(po) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4*>(po + 4) = make_float4(x[4], x[5], x[6], x[7]);
+        } else {
+            const float inv = m == -__builtin_inff() ? 0.0f : 1.0f / l;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) x[u] *= inv;
+            const uint32_t rt = p.by_g.div(row0 + row);
+            const uint32_t head = w.hk * p.by_g.d + (row0 + row - rt * p.by_g.d);
+            const uint32_t si = p.by_tq.div(rt);
+            const int64_t seq = (int64_t)w.eb * p.share + si;
+            uint16_t* op = p.o + seq * p.o_sb + (int64_t)(rt - si * p.by_tq.d) * p.o_st + (int64_t)head * p.o_sh;
+            *reinterpret_cast<uint4*>(op + c) = pack8<T>(x);
+        }
+    }
+#endif
+}
+
+// The splits of one row joined, in order: 8 teams of 32 lanes take every eighth
+// split (4 channels a lane), then the teams' sums are added.
+template <typename T>
+__global__ __launch_bounds__(256) void join_kernel(Params p)
+{
+    __shared__ float4 acc[8][32];
+    __shared__ float sums[8];
+    const uint32_t team = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint64_t first = (uint64_t)blockIdx.x * p.splits;
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + first;
+    float m = -__builtin_inff();
+    for (uint32_t s = lane; s < p.splits; s += 32) m = fmaxf(m, ml[s].x);
+    m = fmaxf(m, dpp_xor<1>(m));
+    m = fmaxf(m, dpp_xor<2>(m));
+    m = fmaxf(m, swizzle_xor<4>(m));
+    m = fmaxf(m, swizzle_xor<8>(m));
+    m = fmaxf(m, swizzle_xor<16>(m));
+    float l = 0.0f;
+    float4 x = make_float4(0, 0, 0, 0);
+    const bool there = lane * 4 < p.d;
+    for (uint32_t s = team; s < p.splits; s += 8) {
+        const float2 t = ml[s];
+        if (t.x == -__builtin_inff()) continue;   // nothing in this split
+        const float f = __builtin_amdgcn_exp2f((t.x - m) * p.c);
+        l = __builtin_fmaf(t.y, f, l);
+        if (!there) continue;
+        const float4 v = *reinterpret_cast<const float4*>(p.part_o + (first + s) * p.d + lane * 4);
+        x.x = __builtin_fmaf(v.x, f, x.x), x.y = __builtin_fmaf(v.y, f, x.y);
+        x.z = __builtin_fmaf(v.z, f, x.z), x.w = __builtin_fmaf(v.w, f, x.w);
+    }
+    acc[team][lane] = x;
+    if (lane == 0) sums[team] = l;
+    __syncthreads();
+    if (team != 0 || !there) return;
+    l = sums[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+        const float4 v = acc[i][lane];
+        l += sums[i];
+        x.x += v.x, x.y += v.y, x.z += v.z, x.w += v.w;
+    }
+    const float inv = m == -__builtin_inff() ? 0.0f : 1.0f / l;
+    const uint32_t bh = p.by_tiles.div(blockIdx.x), row = blockIdx.x - bh * p.rows;   // by_tiles: by rows here
+    const uint32_t eb = p.by_hkv.div(bh), hk = bh - eb * p.heads_kv;
+    const uint32_t rt = p.by_g.div(row), head = hk * p.by_g.d + (row - rt * p.by_g.d);
+    const uint32_t si = p.by_tq.div(rt);
+    const int64_t seq = (int64_t)eb * p.share + si;
+    uint16_t* op = p.o + seq * p.o_sb + (int64_t)(rt - si * p.by_tq.d) * p.o_st + (int64_t)head * p.o_sh;
+    *reinterpret_cast<uint2*>(op + lane * 4) = make_uint2(pack2<T>(x.x * inv, x.y * inv), pack2<T>(x.z * inv, x.w * inv));
 }
 
 }  // namespace attn
 
 namespace {
 
-template <typename T, int DP, int NW>
-hipError_t launch(attn::Params p, uint32_t bh, hipStream_t st)
+// How a call runs: by slices (few rows) or tiles, and over how many splits.
+struct Plan {
+    bool slices;
+    uint32_t m_tiles, splits, split_keys;
+};
+
+constexpr int kTileWaves = 4;
+
+Plan plan_of(int64_t bh, int64_t rows, int64_t tk)
 {
-    p.m_tiles = (p.rows + 32 * NW - 1) / (32 * NW);
-    p.by_tiles = FastDiv(p.m_tiles);
-    attn::tile_kernel<T, DP, NW><<<dim3(bh * p.m_tiles), dim3(NW * 64), 0, st>>>(p);
+    Plan p{};
+    p.slices = rows <= 96;
+    const int64_t tile_rows = p.slices ? 32 : 32 * kTileWaves;
+    p.m_tiles = (uint32_t)((rows + tile_rows - 1) / tile_rows);
+    const int64_t groups = bh * p.m_tiles, want = 2 * (int64_t)num_cus();
+    const int64_t least = p.slices ? 256 : 512;   // keys worth a workgroup
+    int64_t splits = std::max<int64_t>(1, std::min((want + groups - 1) / groups, tk / least));
+    if (groups >= num_cus()) splits = 1;
+    const int64_t unit = 128;
+    const int64_t keys = (tk + splits - 1) / splits;
+    p.split_keys = (uint32_t)std::max<int64_t>(unit, (keys + unit - 1) / unit * unit);
+    p.splits = (uint32_t)std::max<int64_t>(1, (tk + p.split_keys - 1) / p.split_keys);
+    return p;
+}
+
+template <typename T, int DP, bool MASK>
+hipError_t launch(attn::Params& p, const Plan& plan, uint32_t bh, hipStream_t st)
+{
+    const dim3 grid(bh * plan.m_tiles * plan.splits);
+    if (plan.slices)
+        attn::slice_kernel<T, DP, MASK><<<grid, dim3(256), 0, st>>>(p);
+    else
+        attn::tile_kernel<T, DP, kTileWaves, MASK><<<grid, dim3(kTileWaves * 64), 0, st>>>(p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || plan.splits == 1) return e;
+    p.by_tiles = FastDiv(p.rows);
+    attn::join_kernel<T><<<dim3(bh * p.rows), dim3(256), 0, st>>>(p);
     return hipGetLastError();
 }
 
-template <typename T>
-hipError_t pick(const attn::Params& p, uint32_t bh, hipStream_t st)
+template <typename T, bool MASK>
+hipError_t pick(attn::Params& p, const Plan& plan, uint32_t bh, hipStream_t st)
 {
-    if (p.d <= 64) return launch<T, 64, 4>(p, bh, st);
-    if (p.d <= 96) return launch<T, 96, 4>(p, bh, st);
-    return launch<T, 128, 4>(p, bh, st);
+    if (p.d <= 64) return launch<T, 64, MASK>(p, plan, bh, st);
+    if (p.d <= 96) return launch<T, 96, MASK>(p, plan, bh, st);
+    return launch<T, 128, MASK>(p, plan, bh, st);
 }
 
 }  // namespace
 
-size_t cross_attn_workspace(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
+size_t cross_attn_workspace(int64_t batch, int64_t kv_batch, int64_t tq, int64_t tk, int64_t heads, int64_t kv_heads,
+                            int64_t d)
+{
+    const int64_t bh = kv_batch * kv_heads, rows = batch / kv_batch * tq * (heads / kv_heads);
+    const Plan p = plan_of(bh, rows, tk);
+    return p.splits == 1 ? 0 : (size_t)(bh * rows * p.splits) * (size_t)(d + 2) * sizeof(float);
+}
 
 hipError_t launch_cross_attn(const AttnArgs& a, hipStream_t st)
 {
@@ -406,8 +731,21 @@ hipError_t launch_cross_attn(const AttnArgs& a, hipStream_t st)
     p.by_g = FastDiv((uint32_t)g);
     p.by_tq = FastDiv((uint32_t)a.tq);
     p.by_hkv = FastDiv((uint32_t)a.kv_heads);
-    const uint32_t bh = (uint32_t)(a.kv_batch * a.kv_heads);
-    return a.fp16 ? pick<f16>(p, bh, st) : pick<bf16>(p, bh, st);
+    const int64_t bh = a.kv_batch * a.kv_heads;
+    const Plan plan = plan_of(bh, p.rows, a.tk);
+    p.m_tiles = plan.m_tiles;
+    p.splits = plan.splits;
+    p.split_keys = plan.split_keys;
+    p.by_tiles = FastDiv(p.m_tiles);
+    p.by_splits = FastDiv(p.splits);
+    // a listed key's offset from the list's first stays below 2^31 bytes
+    const int64_t pitch = std::max<int64_t>(1, std::max(a.k_st, a.v_st)) * 2;
+    p.list_keys = (uint32_t)std::min<int64_t>(attn::kList, 0x7f000000LL / pitch);
+    p.part_o = static_cast<float*>(a.ws);
+    p.part_ml = p.part_o + (uint64_t)bh * p.rows * p.splits * p.d;
+    if (a.mask)
+        return a.fp16 ? pick<f16, true>(p, plan, (uint32_t)bh, st) : pick<bf16, true>(p, plan, (uint32_t)bh, st);
+    return a.fp16 ? pick<f16, false>(p, plan, (uint32_t)bh, st) : pick<bf16, false>(p, plan, (uint32_t)bh, st);
 }
 
 }  // namespace ck
