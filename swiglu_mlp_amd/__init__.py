@@ -686,8 +686,8 @@ _PACK_HEADS, _PACK_SIDE = struct.Struct("4Q"), struct.Struct("17Q")
 def _heads(t, what, dtype, dev):
     """Check a [batch, tokens, heads, d] tensor of 16-bit values; returns the
     words of its ck_heads (address, batch, token and head strides).  dev: the
-    device index the call runs on."""
-    if t.dtype is not dtype or not t.is_cuda or t.get_device() != dev or t.dim() != 4:
+    device index the call runs on (a CPU tensor's is -1)."""
+    if t.dtype is not dtype or t.get_device() != dev or t.dim() != 4:
         raise ValueError(f"{what} needs a {dtype} [batch, tokens, heads, d] tensor on cuda:{dev}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     (b, n, h, d), (sb, sn, sh, sd) = t.shape, t.stride()
@@ -762,37 +762,40 @@ def _heads_out(out, like, words, what, others, in_place, dtype, dev):
     return out, at
 
 
-def _qk_side(x, y, weight, rope, pos, d, half, what, dev):
-    """One side's ck_qk_side (include/ck.h), packed; x and y: ck_heads words."""
+def _rope(rope, half, what, dev):
+    """(cos address, sin address, rows) of a side's rotation tables."""
     import torch
-    b, n, h = x[1]
-    w = cos_p = sin_p = rows = pos_p = pos_st = 0
+    cos, sin = rope
+    shape = cos.shape
+    if (cos.dtype is not torch.float32 or sin.dtype is not torch.float32 or len(shape) != 2 or shape[1] != half
+            or sin.shape != shape or cos.get_device() != dev or sin.get_device() != dev
+            or not cos.is_contiguous() or not sin.is_contiguous()):
+        raise ValueError(f"{what}_rope needs contiguous float32 [rows, {half}] cos and sin of one shape on cuda:{dev}")
+    return cos.data_ptr(), sin.data_ptr(), shape[0]
+
+
+def _qk_side(words, sizes, out_words, weight, rope, pos, d, what, dev):
+    """One side's ck_qk_side (include/ck.h), packed; rope: from _rope, or None."""
+    import torch
+    b, n, h = sizes
+    w = cos = sin = rows = pos_p = pos_st = 0
     if weight is not None:
-        if (weight.dtype is not torch.float32 or weight.shape != (d,) or not weight.is_cuda
-                or weight.get_device() != dev or not weight.is_contiguous()):
+        if (weight.dtype is not torch.float32 or weight.shape != (d,) or weight.get_device() != dev
+                or not weight.is_contiguous()):
             raise ValueError(f"{what}_weight needs a contiguous float32 ({d},) tensor on cuda:{dev}")
         w = weight.data_ptr()
     if rope is not None:
-        cos, sin = rope
-        for t in rope:
-            if (t.dtype is not torch.float32 or t.dim() != 2 or t.shape[1] != half or not t.is_cuda
-                    or t.get_device() != dev or not t.is_contiguous()):
-                raise ValueError(f"{what}_rope needs contiguous float32 [rows, {half}] cos and sin on cuda:{dev}")
-        rows = cos.shape[0]
-        if sin.shape[0] != rows:
-            raise ValueError(f"{what}_rope needs cos and sin of one shape")
-        cos_p, sin_p = cos.data_ptr(), sin.data_ptr()
-        if pos is None:
-            if n > rows:
-                raise ValueError(f"{what}_rope has {rows} rows for {n} tokens")
-        else:
-            if (pos.dtype is not torch.int32 or pos.shape != (b, n) or not pos.is_cuda or pos.get_device() != dev
+        cos, sin, rows = rope
+        if pos is not None:
+            if (pos.dtype is not torch.int32 or pos.shape != (b, n) or pos.get_device() != dev
                     or (n > 1 and pos.stride(1) != 1)):
                 raise ValueError(f"{what}_pos needs an int32 ({b}, {n}) tensor with contiguous rows on cuda:{dev}")
             pos_p, pos_st = pos.data_ptr(), pos.stride(0) if b > 1 else 0
+        elif n > rows:
+            raise ValueError(f"{what}_rope has {rows} rows for {n} tokens")
     elif pos is not None:
         raise ValueError(f"{what}_pos without {what}_rope")
-    return _PACK_SIDE.pack(*x[0], *y, b, n, h, w, cos_p, sin_p, rows, pos_p, pos_st)
+    return _PACK_SIDE.pack(*words, *out_words, b, n, h, w, cos, sin, rows, pos_p, pos_st)
 
 
 def ck_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, q_rope=None, k_rope=None, q_pos=None,
@@ -812,21 +815,25 @@ def ck_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, q_rope=None, k_rope
     code, dtype, dev = _first(q, "q")
     hq = _heads(q, "q", dtype, dev)
     *q_sizes, d = q.shape
-    half = 0
-    for rope in (q_rope, k_rope):
-        if rope is not None:
-            if not isinstance(rope, (tuple, list)) or len(rope) != 2:
-                raise ValueError("a rope is (cos, sin)")
-            if half and rope[0].shape[-1] != half:
-                raise ValueError("q_rope and k_rope turn different numbers of channels")
-            half = rope[0].shape[-1]
-    if 2 * half > d or half % (8 if pairing == "half" else 4):
-        raise ValueError(f"the rotated channels must be a multiple of {16 if pairing == 'half' else 8} up to {d}, "
-                         f"got {2 * half}")
     if d > 256:
         raise ValueError(f"head size {d} is over 256")
+    half = 0
+    tq = tk = None
+    first = q_rope if q_rope is not None else k_rope
+    if first is not None:
+        for rope in (q_rope, k_rope):
+            if rope is not None and (not isinstance(rope, (tuple, list)) or len(rope) != 2):
+                raise ValueError("a rope is (cos, sin)")
+        half = first[0].shape[-1]
+        if 2 * half > d or half % (8 if pairing == "half" else 4):
+            raise ValueError(f"the rotated channels must be a multiple of {16 if pairing == 'half' else 8} up to {d}, "
+                             f"got {2 * half}")
+        if q_rope is not None:
+            tq = _rope(q_rope, half, "q", dev)
+        if k_rope is not None:
+            tk = tq if k_rope is q_rope else _rope(k_rope, half, "k", dev)
     y, hy = _heads_out(q_out, q, hq, "q_out", () if k is None else (k,), True, dtype, dev)
-    side_q = _qk_side((hq, q_sizes), hy, q_weight, q_rope, q_pos, d, half, "q", dev)
+    side_q = _qk_side(hq, q_sizes, hy, q_weight, tq, q_pos, d, "q", dev)
     z = side_k = None
     if k is not None:
         hk = _heads(k, "k", dtype, dev)
@@ -836,7 +843,7 @@ def ck_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, q_rope=None, k_rope
         z, hz = _heads_out(k_out, k, hk, "k_out", (q,), True, dtype, dev)
         if q_out is not None and k_out is not None and not _disjoint(y, z):
             raise ValueError("q_out and k_out must not share memory")
-        side_k = _qk_side((hk, k_sizes), hz, k_weight, k_rope, k_pos, d, half, "k", dev)
+        side_k = _qk_side(hk, k_sizes, hz, k_weight, tk, k_pos, d, "k", dev)
     elif k_weight is not None or k_rope is not None or k_pos is not None or k_out is not None:
         raise ValueError("arguments for k without k")
     _call("ck_qk_norm_rope", side_q, side_k, d, 2 * half, _PAIRING[pairing], code, eps, _raw_stream(dev))
@@ -870,20 +877,24 @@ def ck_cross_attn(q, k, v, scale=None, kv_len=None, key_mask=None, out=None, wor
     len_p = mask_p = ws_p = None
     mask_st = ws_n = 0
     if kv_len is not None:
-        if (kv_len.dtype is not torch.int32 or kv_len.shape != (kb,) or not kv_len.is_cuda
-                or kv_len.get_device() != dev or not kv_len.is_contiguous()):
+        if (kv_len.dtype is not torch.int32 or kv_len.shape != (kb,) or kv_len.get_device() != dev
+                or not kv_len.is_contiguous()):
             raise ValueError(f"kv_len needs a contiguous int32 ({kb},) tensor on cuda:{dev}")
         len_p = kv_len.data_ptr()
     if key_mask is not None:
-        if (key_mask.dtype not in (torch.bool, torch.uint8) or key_mask.shape != (kb, tk) or not key_mask.is_cuda
+        if (key_mask.dtype not in (torch.bool, torch.uint8) or key_mask.shape != (kb, tk)
                 or key_mask.get_device() != dev or (tk > 1 and key_mask.stride(1) != 1)):
             raise ValueError(f"key_mask needs a bool or uint8 ({kb}, {tk}) tensor with contiguous rows on cuda:{dev}")
         mask_p, mask_st = key_mask.data_ptr(), key_mask.stride(0) if kb > 1 else 0
     y, hy = _heads_out(out, q, hq, "out", (k, v), False, dtype, dev)
     need = lib().ck_cross_attn_workspace_size(b, kb, tq, tk, h, kh, d)
     if need:
-        ws = _workspace(workspace, need, q.device)
-        ws_p, ws_n = ws.data_ptr(), ws.numel()
+        if workspace is None:
+            workspace = q.new_empty((need // 2,))
+            ws_n = need
+        else:
+            ws_n = _workspace(workspace, need, q.device).numel()
+        ws_p = workspace.data_ptr()
     pack = _PACK_HEADS.pack
     _call("ck_cross_attn", pack(*hq), pack(*hk), pack(*hv), pack(*hy), b, kb, tq, tk, h, kh, d, code, scale,
           len_p, mask_p, mask_st, ws_p, ws_n, _raw_stream(dev))

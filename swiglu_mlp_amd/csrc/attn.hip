@@ -164,18 +164,28 @@ struct Place {
     int64_t q_at, o_at;        // element offsets of the row
 };
 
-// Workgroup index -> (key head, row tile, split); rows tiles of 32 `waves`.
-__device__ __forceinline__ Place place_of(const Params& p, uint32_t block, uint32_t row_in_tile, uint32_t tile_rows)
+// Workgroup index -> (key head, split, row tile), the row tiles of one split
+// next to each other.  Workgroups go to the 8 XCDs (each with an L2 of its own)
+// in turn: without lengths each XCD takes a contiguous eighth of the order, so
+// the row tiles that read the same keys share an L2.  With lengths the plain
+// order stays, which spreads a long sequence over the XCDs.
+__device__ __forceinline__ Place place_of(const Params& p, uint32_t row_in_tile, uint32_t tile_rows)
 {
     Place w;
     const uint32_t lane = threadIdx.x & 63;
     w.half = lane >> 5, w.col = lane & 31;
-    const uint32_t rest = p.by_splits.div(block);
-    w.split = block - rest * p.splits;
-    w.bh = p.by_tiles.div(rest);
+    uint32_t at = blockIdx.x;
+    if (!p.kv_len) {
+        const uint32_t x = at & 7u, all = gridDim.x;
+        at = x * (all >> 3) + min(x, all & 7u) + (at >> 3);
+    }
+    const uint32_t rest = p.by_tiles.div(at);
+    const uint32_t mt = at - rest * p.m_tiles;
+    w.bh = p.by_splits.div(rest);
+    w.split = rest - w.bh * p.splits;
     w.eb = p.by_hkv.div(w.bh);
     w.hk = w.bh - w.eb * p.heads_kv;
-    w.row = (rest - w.bh * p.m_tiles) * tile_rows + row_in_tile + w.col;
+    w.row = mt * tile_rows + row_in_tile + w.col;
     const uint32_t r = w.row < p.rows ? w.row : p.rows - 1;   // rows past the last compute the last, and store nothing
     const uint32_t rt = p.by_g.div(r);
     const uint32_t head = w.hk * p.by_g.d + (r - rt * p.by_g.d);
@@ -415,7 +425,7 @@ __global__ __launch_bounds__(NW * 64, 2) void tile_kernel(Params p)
     __shared__ uint32_t counts[NW];
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const Place w = place_of(p, blockIdx.x, wave * 32, NW * 32);
+    const Place w = place_of(p, wave * 32, NW * 32);
     v4u q[DP / 16];
     load_q<DP>(p, w, q);
     Loader<DP, NK, PER, MASK> ld;
@@ -502,7 +512,7 @@ __global__ __launch_bounds__(256, 1) void slice_kernel(Params p)
     __shared__ float2 ml[NW][32];
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const Place w = place_of(p, blockIdx.x, 0, 32);
+    const Place w = place_of(p, 0, 32);
     v4u q[DP / 16];
     load_q<DP>(p, w, q);
     Loader<DP, NK, PER, MASK> ld;
@@ -597,15 +607,19 @@ __global__ __launch_bounds__(256, 1) void slice_kernel(Params p)
 #endif
 }
 
-// The splits of one row joined, in order: 8 teams of 32 lanes take every eighth
-// split (4 channels a lane), then the teams' sums are added.
-template <typename T>
-__global__ __launch_bounds__(256) void join_kernel(Params p)
+// The splits of a row joined, in a fixed order, 4 channels a lane.  TEAMS teams
+// of 32 lanes share a row: one where there are many rows of few splits, eight
+// (each every eighth split, then added) where there are few rows of many.
+template <typename T, int TEAMS>
+__global__ __launch_bounds__(256) void join_kernel(Params p, uint32_t all_rows)
 {
-    __shared__ float4 acc[8][32];
+    constexpr int ROWS = 8 / TEAMS;   // per workgroup
+    __shared__ float4 acc[TEAMS == 1 ? 1 : 8][32];
     __shared__ float sums[8];
     const uint32_t team = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const uint64_t first = (uint64_t)blockIdx.x * p.splits;
+    const uint32_t at = blockIdx.x * ROWS + team / TEAMS, own = team % TEAMS;
+    const bool there = lane * 4 < p.d && at < all_rows;
+    const uint64_t first = (uint64_t)min(at, all_rows - 1) * p.splits;
     const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + first;
     float m = -__builtin_inff();
     for (uint32_t s = lane; s < p.splits; s += 32) m = fmaxf(m, ml[s].x);
@@ -616,30 +630,33 @@ __global__ __launch_bounds__(256) void join_kernel(Params p)
     m = fmaxf(m, swizzle_xor<16>(m));
     float l = 0.0f;
     float4 x = make_float4(0, 0, 0, 0);
-    const bool there = lane * 4 < p.d;
-    for (uint32_t s = team; s < p.splits; s += 8) {
+#pragma unroll 4
+    for (uint32_t s = own; s < p.splits; s += TEAMS) {
         const float2 t = ml[s];
-        if (t.x == -__builtin_inff()) continue;   // nothing in this split
-        const float f = __builtin_amdgcn_exp2f((t.x - m) * p.c);
+        float4 v = make_float4(0, 0, 0, 0);
+        // a split without keys has written its m (-inf) and l, and zeros
+        if (there) v = *reinterpret_cast<const float4*>(p.part_o + (first + s) * p.d + lane * 4);
+        const float f = t.x == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f((t.x - m) * p.c);
         l = __builtin_fmaf(t.y, f, l);
-        if (!there) continue;
-        const float4 v = *reinterpret_cast<const float4*>(p.part_o + (first + s) * p.d + lane * 4);
         x.x = __builtin_fmaf(v.x, f, x.x), x.y = __builtin_fmaf(v.y, f, x.y);
         x.z = __builtin_fmaf(v.z, f, x.z), x.w = __builtin_fmaf(v.w, f, x.w);
     }
-    acc[team][lane] = x;
-    if (lane == 0) sums[team] = l;
-    __syncthreads();
-    if (team != 0 || !there) return;
-    l = sums[0];
+    if constexpr (TEAMS > 1) {
+        acc[team][lane] = x;
+        if (lane == 0) sums[team] = l;
+        __syncthreads();
+        if (team != 0) return;
+        l = sums[0];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) {
-        const float4 v = acc[i][lane];
-        l += sums[i];
-        x.x += v.x, x.y += v.y, x.z += v.z, x.w += v.w;
+        for (int i = 1; i < TEAMS; ++i) {
+            const float4 v = acc[i][lane];
+            l += sums[i];
+            x.x += v.x, x.y += v.y, x.z += v.z, x.w += v.w;
+        }
     }
+    if (!there) return;
     const float inv = m == -__builtin_inff() ? 0.0f : 1.0f / l;
-    const uint32_t bh = p.by_tiles.div(blockIdx.x), row = blockIdx.x - bh * p.rows;   // by_tiles: by rows here
+    const uint32_t bh = p.by_tiles.div(at), row = at - bh * p.rows;   // by_tiles: by rows here
     const uint32_t eb = p.by_hkv.div(bh), hk = bh - eb * p.heads_kv;
     const uint32_t rt = p.by_g.div(row), head = hk * p.by_g.d + (row - rt * p.by_g.d);
     const uint32_t si = p.by_tq.div(rt);
@@ -660,16 +677,20 @@ struct Plan {
 
 constexpr int kTileWaves = 4;
 
-Plan plan_of(int64_t bh, int64_t rows, int64_t tk)
+Plan plan_of(int64_t bh, int64_t rows, int64_t tk, int64_t d)
 {
     Plan p{};
     p.slices = rows <= 96;
     const int64_t tile_rows = p.slices ? 32 : 32 * kTileWaves;
     p.m_tiles = (uint32_t)((rows + tile_rows - 1) / tile_rows);
-    const int64_t groups = bh * p.m_tiles, want = 2 * (int64_t)num_cus();
-    const int64_t least = p.slices ? 256 : 512;   // keys worth a workgroup
-    int64_t splits = std::max<int64_t>(1, std::min((want + groups - 1) / groups, tk / least));
-    if (groups >= num_cus()) splits = 1;
+    // As many splits as keep every workgroup resident at once (a slice workgroup
+    // of up to 64 channels takes under half of a CU's LDS): a second round of
+    // workgroups costs more than it balances, also where lengths differ.  A
+    // split below one slice a wave is not worth its join.
+    const int64_t groups = bh * p.m_tiles, cus = num_cus();
+    const int64_t resident = cus * (p.slices && d > 64 ? 1 : 2), least = p.slices ? 128 : 512;
+    int64_t splits = std::max<int64_t>(1, std::min(resident / groups, tk / least));
+    if (!p.slices && groups >= cus) splits = 1;
     const int64_t unit = 128;
     const int64_t keys = (tk + splits - 1) / splits;
     p.split_keys = (uint32_t)std::max<int64_t>(unit, (keys + unit - 1) / unit * unit);
@@ -688,7 +709,11 @@ hipError_t launch(attn::Params& p, const Plan& plan, uint32_t bh, hipStream_t st
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || plan.splits == 1) return e;
     p.by_tiles = FastDiv(p.rows);
-    attn::join_kernel<T><<<dim3(bh * p.rows), dim3(256), 0, st>>>(p);
+    const uint32_t rows = bh * p.rows;
+    if (plan.splits >= 16)
+        attn::join_kernel<T, 8><<<dim3(rows), dim3(256), 0, st>>>(p, rows);
+    else
+        attn::join_kernel<T, 1><<<dim3((rows + 7) / 8), dim3(256), 0, st>>>(p, rows);
     return hipGetLastError();
 }
 
@@ -706,7 +731,7 @@ size_t cross_attn_workspace(int64_t batch, int64_t kv_batch, int64_t tq, int64_t
                             int64_t d)
 {
     const int64_t bh = kv_batch * kv_heads, rows = batch / kv_batch * tq * (heads / kv_heads);
-    const Plan p = plan_of(bh, rows, tk);
+    const Plan p = plan_of(bh, rows, tk, d);
     return p.splits == 1 ? 0 : (size_t)(bh * rows * p.splits) * (size_t)(d + 2) * sizeof(float);
 }
 
@@ -732,7 +757,7 @@ hipError_t launch_cross_attn(const AttnArgs& a, hipStream_t st)
     p.by_tq = FastDiv((uint32_t)a.tq);
     p.by_hkv = FastDiv((uint32_t)a.kv_heads);
     const int64_t bh = a.kv_batch * a.kv_heads;
-    const Plan plan = plan_of(bh, p.rows, a.tk);
+    const Plan plan = plan_of(bh, p.rows, a.tk, a.d);
     p.m_tiles = plan.m_tiles;
     p.splits = plan.splits;
     p.split_keys = plan.split_keys;
