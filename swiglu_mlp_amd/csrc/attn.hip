@@ -81,7 +81,9 @@ template <int N>
 __device__ __forceinline__ void wait_vmcnt()
 {
     static_assert(N >= 0 && N < 64, "vmcnt range");
+    asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+    asm volatile("" ::: "memory");
 }
 
 // s_barrier without a fence; the empty asm statements keep memory accesses on
@@ -196,7 +198,9 @@ __device__ __forceinline__ Place place_of(const Params& p, uint32_t row_in_tile,
     w.o_at = seq * p.o_sb + (int64_t)tok * p.o_st + (int64_t)head * p.o_sh;
     uint32_t len = p.tk;
     if (p.kv_len) {
-        const int32_t l = p.kv_len[w.eb];
+        // through the scalar cache: nothing in this launch writes lengths
+        typedef const __attribute__((address_space(4))) int32_t* Lens;
+        const int32_t l = ((Lens)p.kv_len)[w.eb];
         len = l < 0 ? 0u : min((uint32_t)l, p.tk);
     }
     w.first = min(w.split * p.split_keys, len);
@@ -204,15 +208,14 @@ __device__ __forceinline__ Place place_of(const Params& p, uint32_t row_in_tile,
     return w;
 }
 
+// The row's fragments.  Chunks past d hold channels of the last one again: K is
+// zero there.  (An infinity or NaN in q makes the row NaN with or without them.)
 template <int DP>
 __device__ __forceinline__ void load_q(const Params& p, const Place& w, v4u (&q)[DP / 16])
 {
 #pragma unroll
-    for (int s = 0; s < DP / 16; ++s) {
-        const uint32_t c = 16 * s + 8 * w.half;
-        q[s] = v4u{0, 0, 0, 0};
-        if (c < p.d) q[s] = *reinterpret_cast<const v4u*>(p.q + w.q_at + c);
-    }
+    for (int s = 0; s < DP / 16; ++s)
+        q[s] = *reinterpret_cast<const v4u*>(p.q + w.q_at + min(16 * s + 8 * w.half, p.d - 8));
 }
 
 // The indices (from `from`) of the allowed keys among [from, from + n), n <=
@@ -254,50 +257,93 @@ __device__ uint32_t list_keys(const uint8_t* mask, uint32_t from, uint32_t n, ui
     return total;
 }
 
-// A wave's loads of 16-byte chunks from rows of K and V into LDS: rows of NK
-// keys of K, then of V; this wave issues loads first .. first + PER - 1.
-// LISTED: the keys come through a list of their indices.
-template <int DP, int NK, int PER, bool LISTED>
+// A wave's loads of a K or V tile of NK keys into LDS: CNT of its NK DP / 512
+// one-KB pieces, from piece `first` on, a 16-byte chunk per lane.  LISTED: the
+// keys come through a list of their indices.
+template <int DP, int NK, int CNT, bool LISTED>
 struct Loader {
-    static constexpr int CH = DP / 8, NI = NK * DP * 2 / 1024;
-    const char *k, *v;           // of key 0 of the head
-    uint32_t k_pitch, v_pitch, d, lane;
-    uint32_t off[PER];           // of this lane's chunk: in its row (LISTED) or in the tile
+    static constexpr int CH = DP / 8;
+    const char* base;      // key 0 of the head
+    uint32_t pitch;        // bytes from key to key
+    uint32_t first, lane;
+    uint32_t off[CNT];     // of this lane's chunk: in its row (LISTED) or in the tile
 
-    __device__ __forceinline__ uint32_t row(int j) const { return ((j < NI ? j : j - NI) * 64 + lane) / CH; }
-    __device__ __forceinline__ uint32_t chunk(int j) const
+    // key of the tile that this lane reads in piece first + i
+    __device__ __forceinline__ uint32_t row(int i) const
     {
-        const uint32_t r = row(j), at = ((j < NI ? j : j - NI) * 64 + lane) % CH;
-        const uint32_t c = j < NI ? k_swz<CH>(r, at) : v_swz<CH>(r, at);   // both are their own inverse
-        return 8 * c < d ? 16 * c : kBufferOutside;
+        if constexpr (64 % CH == 0) return lane / CH + (first + i) * (64 / CH);
+        return ((first + i) * 64 + lane) / CH;
     }
-    __device__ __forceinline__ void init(const Params& p, const Place& w, int first)
+    __device__ __forceinline__ bool past(int i, uint32_t left) const   // row(i) >= left
     {
+        if constexpr (64 % CH == 0) return (int)(lane / CH) >= (int)(left - (first + i) * (64 / CH));
+        return row(i) >= left;
+    }
+    __device__ __forceinline__ void init(const Params& p, const Place& w, bool is_v, uint32_t first_piece)
+    {
+        base = reinterpret_cast<const char*>(is_v ? p.v + (int64_t)w.eb * p.v_sb + (int64_t)w.hk * p.v_sh
+                                                  : p.k + (int64_t)w.eb * p.k_sb + (int64_t)w.hk * p.k_sh);
+        pitch = (uint32_t)((is_v ? p.v_st : p.k_st) * 2);
+        first = first_piece;
         lane = threadIdx.x & 63;
-        d = p.d;
-        k = reinterpret_cast<const char*>(p.k + (int64_t)w.eb * p.k_sb + (int64_t)w.hk * p.k_sh);
-        v = reinterpret_cast<const char*>(p.v + (int64_t)w.eb * p.v_sb + (int64_t)w.hk * p.v_sh);
-        k_pitch = (uint32_t)(p.k_st * 2), v_pitch = (uint32_t)(p.v_st * 2);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            off[i] = chunk(first + i);   // past d: 2^31, and past the buffer with any row's offset added
-            if constexpr (!LISTED) off[i] += row(first + i) * (first + i < NI ? k_pitch : v_pitch);
+        for (int i = 0; i < CNT; ++i) {
+            const uint32_t r = row(i), at = ((first + i) * 64 + lane) % CH;
+            const uint32_t c = is_v ? v_swz<CH>(r, at) : k_swz<CH>(r, at);   // both are their own inverse
+            // a chunk past d: 2^31, and past the buffer with any row's offset added
+            off[i] = (8 * c < p.d ? 16 * c : kBufferOutside) + (LISTED ? 0 : r * pitch);
         }
     }
-    // keys key .. key + NK - 1, or key + list[0 .. NK - 1]; only the first
-    // `left` are there
-    __device__ __forceinline__ void load(uint32_t key, const uint16_t* list, uint32_t left, int first,
-                                         uint32_t lds) const
+    // keys key .. key + NK - 1, or key + list[0 .. NK - 1], to the tile at LDS
+    // address lds; only the first `left` are there
+    __device__ __forceinline__ void load(uint32_t key, const uint16_t* list, uint32_t left, uint32_t lds) const
     {
-        const v4i rk = make_rsrc(k + (uint64_t)key * k_pitch), rv = make_rsrc(v + (uint64_t)key * v_pitch);
+        const v4i rsrc = make_rsrc(base + (uint64_t)key * pitch);
+        if (!LISTED && left >= (uint32_t)NK) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int j = first + i;
-            uint32_t at = off[i];
-            if constexpr (LISTED) at += list[min(row(j), left - 1)] * (j < NI ? k_pitch : v_pitch);
-            if (left < (uint32_t)NK && row(j) >= left) at = kBufferOutside;
-            lds_dma_b128(j < NI ? rk : rv, at, lds + j * 1024);
+            for (int i = 0; i < CNT; ++i) lds_dma_b128(rsrc, off[i], lds + (first + i) * 1024);
+        } else {
+            uint32_t at[CNT];
+#pragma unroll
+            for (int i = 0; i < CNT; ++i) {
+                at[i] = off[i];
+                // the list's entries past its end are old ones, and not used
+                if constexpr (LISTED) at[i] += __umul24(list[row(i)], pitch);
+                if (past(i, left)) at[i] = kBufferOutside;
+            }
+#pragma unroll
+            for (int i = 0; i < CNT; ++i) lds_dma_b128(rsrc, at[i], lds + (first + i) * 1024);
         }
+    }
+};
+
+typedef const __attribute__((address_space(3))) char* LdsPtr;
+
+// A lane's places in a K tile (its fragment of 16 channels of row col) and in
+// the V tile behind it (its 8 bytes of the transposing reads of 32 channels).
+// Buffers and rows are constant offsets from these, so a tile's reads cost no
+// address arithmetic.
+template <int DP>
+struct Reads {
+    static constexpr int CH = DP / 8;
+    LdsPtr k[DP / 16], v[DP / 32];
+    __device__ __forceinline__ Reads(const char* base, uint32_t v_behind, uint32_t half, uint32_t col)
+    {
+        const LdsPtr p = (LdsPtr)base;
+#pragma unroll
+        for (int s = 0; s < DP / 16; ++s) k[s] = p + (col * CH + k_swz<CH>(col, 2 * s + half)) * 16;
+        const uint32_t lane = half * 32 + col, j = lane & 15;
+        const uint32_t key = 4 * half + (j >> 2), c = 2 * ((lane >> 4) & 1) + ((j & 3) >> 1);
+#pragma unroll
+        for (int b = 0; b < DP / 32; ++b)
+            v[b] = p + v_behind + (key * CH + v_swz<CH>(key, 4 * b + c)) * 16 + 8 * (j & 1);
+    }
+    __device__ __forceinline__ void move(int by)
+    {
+#pragma unroll
+        for (int s = 0; s < DP / 16; ++s) k[s] += by;
+#pragma unroll
+        for (int b = 0; b < DP / 32; ++b) v[b] += by;
     }
 };
 
@@ -322,29 +368,51 @@ struct Row {
             for (int i = 0; i < 16; ++i) o[b][i] = 0.0f;
     }
 
-    // 32 N keys in LDS (K rows at kb, V rows at vb), the first `left` of them
-    // real.
-    template <int N>
-    __device__ __forceinline__ void step(const char* kb, const char* vb, const v4u (&q)[KS], uint32_t left, float c,
-                                         uint32_t half, uint32_t col)
+    __device__ __forceinline__ static v4u k_read(LdsPtr at)
+    {
+        typedef const __attribute__((address_space(3))) v4u* LdsV4u;
+        return *(LdsV4u)at;
+    }
+    __device__ __forceinline__ static v4u v_read(LdsPtr at)   // keys .. + 3 and + 8 .. + 11
+    {
+        typedef __attribute__((address_space(3))) v4s* LdsV4s;
+        const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsV4s)at);
+        const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsV4s)(at + 8 * CH * 16));
+        return __builtin_bit_cast(v4u, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+
+    // 32 N keys in LDS, AT bytes behind the places `rd`, the first `left` of
+    // them real.  The order of the source is kept (sched_barrier): a fragment
+    // is read a whole block of products before its use, the first V fragments
+    // before the softmax, and the exponentials of the second 32 keys are spread
+    // over the products with the first 32.
+    template <int N, int AT>
+    __device__ __forceinline__ void step(const Reads<DP>& rd, const v4u (&q)[KS], uint32_t left, float c, uint32_t half)
     {
         v16f s[N];
+        v4u kf[KS], vf[DB];
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) kf[ks] = k_read(rd.k[ks] + AT);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int n = 0; n < N; ++n) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[n][i] = 0.0f;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                const uint32_t at = ((col + n * 32) * CH + k_swz<CH>(col, 2 * ks + half)) * 16;
-                s[n] = mfma<T>(*reinterpret_cast<const v4u*>(kb + at), q[ks], s[n]);
+                s[n] = mfma<T>(kf[ks], q[ks], s[n]);
+                if (n + 1 < N) kf[ks] = k_read(rd.k[ks] + (AT + (n + 1) * 32 * CH * 16));
+                if (n + 1 == N && ks >= KS - DB) vf[ks - (KS - DB)] = v_read(rd.v[ks - (KS - DB)] + AT);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
         if (left < 32u * N) {
+            const int end = (int)left - 4 * (int)half;   // one register against constants
 #pragma unroll
             for (int n = 0; n < N; ++n)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    if (n * 32 + (i & 3) + 8 * (i >> 2) + 4 * half >= left) s[n][i] = -__builtin_inff();
+                    if (n * 32 + (i & 3) + 8 * (i >> 2) >= end) s[n][i] = -__builtin_inff();
         }
         float mx = s[0][0];
 #pragma unroll
@@ -366,35 +434,35 @@ struct Row {
                 for (int i = 0; i < 16; ++i) o[b][i] *= alpha;
         }
         const float shift = (m == -__builtin_inff() ? 0.0f : -m * c) + kLift;
-        v4u pf[2 * N];
+        float la = 0.0f, lb = 0.0f;
+        uint32_t pw[N][8];   // probabilities of keys 2 w, 2 w + 1 of block n
+        auto weigh = [&](int n, int w) {
+            const float a = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][2 * w], c, shift));
+            const float b = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][2 * w + 1], c, shift));
+            la += a;
+            lb += b;
+            pw[n][w] = pack2<T>(a, b);
+        };
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            float e[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][i], c, shift));
-            float sum[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sum[i] = (e[i] + e[i + 4]) + (e[i + 8] + e[i + 12]);
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-#pragma unroll
-            for (int g = 0; g < 2; ++g)
-                pf[2 * n + g] = v4u{pack2<T>(e[8 * g], e[8 * g + 1]), pack2<T>(e[8 * g + 2], e[8 * g + 3]),
-                                    pack2<T>(e[8 * g + 4], e[8 * g + 5]), pack2<T>(e[8 * g + 6], e[8 * g + 7])};
-        }
-        const uint32_t lane = half * 32 + col, j16 = lane & 15;
-        const uint32_t v_key = 4 * half + (j16 >> 2), v_chunk = 2 * ((lane >> 4) & 1) + ((j16 & 3) >> 1);
+        for (int w = 0; w < 8; ++w) weigh(0, w);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int g = 0; g < 2 * N; ++g) {
+            const v4u pf = {pw[g / 2][4 * (g % 2)], pw[g / 2][4 * (g % 2) + 1], pw[g / 2][4 * (g % 2) + 2],
+                            pw[g / 2][4 * (g % 2) + 3]};
 #pragma unroll
             for (int b = 0; b < DB; ++b) {
-                typedef __attribute__((address_space(3))) v4s lds_v4s;
-                const uint32_t at = ((v_key + 16 * g) * CH + v_swz<CH>(v_key, 4 * b + v_chunk)) * 16 + 8 * (j16 & 1);
-                const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(vb + at));
-                const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(vb + at + 8 * CH * 16));
-                const v8s a = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-                o[b] = mfma<T>(__builtin_bit_cast(v4u, a), pf[g], o[b]);
+                o[b] = mfma<T>(vf[b], pf, o[b]);
+                if (g + 1 < 2 * N) vf[b] = v_read(rd.v[b] + (AT + (g + 1) * 16 * CH * 16));
+                if (g < 2 && N > 1) {   // product g DB + b of the 2 DB: its share of the 8 pairs
+                    const int i = g * DB + b;
+#pragma unroll
+                    for (int w = 8 * i / (2 * DB); w < 8 * (i + 1) / (2 * DB); ++w) weigh(N - 1, w);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
+        l += la + lb;
     }
 
     // After the last step: the row's whole sum, and the marks of a row without
@@ -413,26 +481,29 @@ struct Row {
 // NW: waves per workgroup, 32 rows each.  Tiles of 64 keys.  MASK: with a key
 // mask (its lists would cost the other calls registers).
 template <typename T, int DP, int NW, bool MASK>
-__global__ __launch_bounds__(NW * 64, 2) void tile_kernel(Params p)
+__global__ __launch_bounds__(NW * 64, DP <= 64 && !MASK ? 4 : 2) void tile_kernel(Params p)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
     constexpr int NK = 64, DB = DP / 32;
     constexpr int TILE_B = NK * DP * 2;              // bytes of one K or V tile
-    constexpr int PER = 2 * TILE_B / 1024 / NW;      // loads (1 KB) of a tile pair per wave
-    static_assert(2 * TILE_B % (1024 * NW) == 0, "loads split evenly over the waves");
+    constexpr int CNT = TILE_B / 1024 / (NW / 2);    // loads of a tile per wave: half of the waves load K, half V
+    static_assert(TILE_B % (1024 * NW / 2) == 0, "loads split evenly over the waves");
     __shared__ __attribute__((aligned(1024))) char smem[2 * 2 * TILE_B];
-    __shared__ uint16_t list[MASK ? kList : 1];
+    __shared__ uint16_t list[MASK ? kList + 64 : 1];
     __shared__ uint32_t counts[NW];
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Place w = place_of(p, wave * 32, NW * 32);
+    Loader<DP, NK, CNT, MASK> ld;
+    ld.init(p, w, wave >= NW / 2, wave % (NW / 2) * CNT);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem + wave / (NW / 2) * TILE_B;
+    const uint8_t* mask = MASK ? p.mask + (int64_t)w.eb * p.mask_sb : nullptr;
+    if constexpr (!MASK)
+        if (w.first < w.last) ld.load(w.first, list, w.last - w.first, lds0);
     v4u q[DP / 16];
     load_q<DP>(p, w, q);
-    Loader<DP, NK, PER, MASK> ld;
-    ld.init(p, w, wave * PER);
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
-    const uint8_t* mask = MASK ? p.mask + (int64_t)w.eb * p.mask_sb : nullptr;
 
+    Reads<DP> rd(smem, TILE_B, w.half, w.col);
     Row<T, DP> r;
     r.clear();
     bool any = false;   // whether any key was allowed (the same for all rows)
@@ -445,15 +516,34 @@ __global__ __launch_bounds__(NW * 64, 2) void tile_kernel(Params p)
         const uint32_t tiles = (n + NK - 1) / NK;
         auto load = [&](uint32_t t) {
             const uint32_t lds = lds0 + (t & 1) * 2 * TILE_B;
-            ld.load(MASK ? from : from + t * NK, list + t * NK, n - t * NK, wave * PER, lds);
+            ld.load(MASK ? from : from + t * NK, list + t * NK, n - t * NK, lds);
         };
-        if (tiles) load(0);
-        for (uint32_t t = 0; t < tiles; ++t) {
-            wait_vmcnt<0>();
-            workgroup_barrier();   // tile t is in LDS, and every wave is done with the other buffer
-            if (t + 1 < tiles) load(t + 1);
-            const char* kb = smem + (t & 1) * 2 * TILE_B;
-            r.template step<2>(kb, kb + TILE_B, q, n - t * NK, p.c, w.half, w.col);
+        if (MASK && tiles) load(0);
+        if constexpr (MASK) {
+            // one loop body, its places moved from buffer to buffer: with two
+            // bodies in two nested loops the accumulators were held twice
+            int other = 2 * TILE_B;
+            for (uint32_t t = 0; t < tiles; ++t) {
+                wait_vmcnt<0>();
+                workgroup_barrier();
+                if (t + 1 < tiles) load(t + 1);
+                r.template step<2, 0>(rd, q, n - t * NK, p.c, w.half);
+                rd.move(other);
+                other = -other;
+            }
+            if (tiles & 1) rd.move(other);   // back to the first buffer
+        } else {
+            for (uint32_t t = 0; t < tiles; ++t) {
+                wait_vmcnt<0>();
+                workgroup_barrier();   // tile t is in LDS, and every wave is done with the other buffer
+                if (t + 1 < tiles) load(t + 1);
+                r.template step<2, 0>(rd, q, n - t * NK, p.c, w.half);
+                if (++t == tiles) break;
+                wait_vmcnt<0>();
+                workgroup_barrier();
+                if (t + 1 < tiles) load(t + 1);
+                r.template step<2, 2 * TILE_B>(rd, q, n - t * NK, p.c, w.half);
+            }
         }
         if constexpr (MASK) workgroup_barrier();   // the list and the buffers are free
         from = upto;
@@ -502,12 +592,12 @@ __global__ __launch_bounds__(256, 1) void slice_kernel(Params p)
 #if defined(__HIP_DEVICE_COMPILE__)
     constexpr int NW = 4, NK = 32, DB = DP / 32;
     constexpr int SLICE_B = NK * DP * 2;             // bytes of one K or V slice
-    constexpr int PER = 2 * SLICE_B / 1024;          // loads (1 KB) per slice pair
+    constexpr int CNT = SLICE_B / 1024;              // loads per slice
     constexpr int PITCH = DP + 4;                    // floats per row of the joined accumulators
     constexpr int RING_B = NW * 2 * 2 * SLICE_B;
     static_assert(RING_B >= NW * 32 * PITCH * 4, "the accumulators of all waves fit the ring");
     __shared__ __attribute__((aligned(1024))) char smem[RING_B];
-    __shared__ uint16_t list[MASK ? kList : 1];
+    __shared__ uint16_t list[MASK ? kList + 64 : 1];
     __shared__ uint32_t counts[NW];
     __shared__ float2 ml[NW][32];
 
@@ -515,9 +605,10 @@ __global__ __launch_bounds__(256, 1) void slice_kernel(Params p)
     const Place w = place_of(p, 0, 32);
     v4u q[DP / 16];
     load_q<DP>(p, w, q);
-    Loader<DP, NK, PER, MASK> ld;
-    ld.init(p, w, 0);
-    const char* mine = smem + wave * (2 * 2 * SLICE_B);
+    Loader<DP, NK, CNT, MASK> lk, lv;
+    lk.init(p, w, false, 0);
+    lv.init(p, w, true, 0);
+    const Reads<DP> rd(smem + wave * (2 * 2 * SLICE_B), SLICE_B, w.half, w.col);
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem + wave * (2 * 2 * SLICE_B);
     const uint8_t* mask = MASK ? p.mask + (int64_t)w.eb * p.mask_sb : nullptr;
 
@@ -531,21 +622,27 @@ __global__ __launch_bounds__(256, 1) void slice_kernel(Params p)
         any |= n != 0;
         const uint32_t slices = (n + NK - 1) / NK;
         auto load = [&](uint32_t t) {
-            const uint32_t lds = lds0 + (t / NW & 1) * 2 * SLICE_B;
-            ld.load(MASK ? from : from + t * NK, list + t * NK, n - t * NK, 0, lds);
+            const uint32_t lds = lds0 + ((t - wave) / NW & 1) * 2 * SLICE_B;
+            lk.load(MASK ? from : from + t * NK, list + t * NK, n - t * NK, lds);
+            lv.load(MASK ? from : from + t * NK, list + t * NK, n - t * NK, lds + SLICE_B);
         };
-        if (wave < slices) load(wave);
-        for (uint32_t t = wave; t < slices; t += NW) {
+        auto wait = [&](uint32_t t) {   // slice t is in LDS; the next one is on its way
             if (t + NW < slices) {
                 load(t + NW);
-                wait_vmcnt<PER>();   // all but the loads just issued: slice t is in LDS
+                wait_vmcnt<2 * CNT>();  // all but the loads just issued
             } else {
                 wait_vmcnt<0>();
             }
-            asm volatile("" ::: "memory");
-            const char* kb = mine + (t / NW & 1) * 2 * SLICE_B;
-            r.template step<1>(kb, kb + SLICE_B, q, n - t * NK, p.c, w.half, w.col);
+        };
+        if (wave < slices) load(wave);
+        for (uint32_t t = wave; t < slices; t += NW) {
+            wait(t);
+            r.template step<1, 0>(rd, q, n - t * NK, p.c, w.half);
             asm volatile("" ::: "memory");   // its LDS reads end before the next load into this buffer
+            if ((t += NW) >= slices) break;
+            wait(t);
+            r.template step<1, 2 * SLICE_B>(rd, q, n - t * NK, p.c, w.half);
+            asm volatile("" ::: "memory");
         }
         if constexpr (MASK) __syncthreads();   // the list is free
         from = upto;
