@@ -478,32 +478,46 @@ struct Row {
 #endif
 
 // DP: channels padded to 64, 96 or 128 (the chunks past d load zeros).
-// NW: waves per workgroup, 32 rows each.  Tiles of 64 keys.  MASK: with a key
-// mask (its lists would cost the other calls registers).
-template <typename T, int DP, int NW, bool MASK>
-__global__ __launch_bounds__(NW * 64, DP <= 64 && !MASK ? 4 : 2) void tile_kernel(Params p)
+// KG key groups of NW waves each: a group's waves hold 32 rows each and share
+// its tiles of 64 keys; the groups hold the same rows, take every KG-th tile,
+// and are joined through LDS at the end.  With KG = 1 two (four for 64
+// channels) workgroups share a CU; KG = 2 fills a CU by itself, for calls with
+// no more workgroups than CUs.  MASK: with a key mask (its lists would cost the
+// other calls registers).
+template <typename T, int DP, int NW, int KG, bool MASK>
+__global__ __launch_bounds__(NW * KG * 64, DP <= 64 && KG == 1 && !MASK ? 4 : 2) void tile_kernel(Params p)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
     constexpr int NK = 64, DB = DP / 32;
     constexpr int TILE_B = NK * DP * 2;              // bytes of one K or V tile
-    constexpr int CNT = TILE_B / 1024 / (NW / 2);    // loads of a tile per wave: half of the waves load K, half V
+    constexpr int CNT = TILE_B / 1024 / (NW / 2);    // loads of a tile per wave: half of a group's waves load K, half V
     static_assert(TILE_B % (1024 * NW / 2) == 0, "loads split evenly over the waves");
-    __shared__ __attribute__((aligned(1024))) char smem[2 * 2 * TILE_B];
+    constexpr int RING_B = 2 * 2 * TILE_B;           // a group's two buffers
+    constexpr int ACC_B = DB * 16 * NW * 64 * 4;     // a group's accumulators
+    static_assert((KG - 1) * ACC_B <= KG * RING_B, "the other groups' accumulators fit the rings");
+    __shared__ __attribute__((aligned(1024))) char smem[KG * RING_B];
     __shared__ uint16_t list[MASK ? kList + 64 : 1];
-    __shared__ uint32_t counts[NW];
+    __shared__ uint32_t counts[NW * KG];
+    __shared__ float2 ml[KG > 1 ? KG - 1 : 1][KG > 1 ? NW * 64 : 1];
 
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int all_wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t group = all_wave / NW;
+    const int wave = all_wave % NW;
     const Place w = place_of(p, wave * 32, NW * 32);
     Loader<DP, NK, CNT, MASK> ld;
     ld.init(p, w, wave >= NW / 2, wave % (NW / 2) * CNT);
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem + wave / (NW / 2) * TILE_B;
+    const char* ring = smem + group * RING_B;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem + group * RING_B +
+                          wave / (NW / 2) * TILE_B;
     const uint8_t* mask = MASK ? p.mask + (int64_t)w.eb * p.mask_sb : nullptr;
-    if constexpr (!MASK)
-        if (w.first < w.last) ld.load(w.first, list, w.last - w.first, lds0);
+    if constexpr (!MASK) {   // before the queries: the longer way
+        const uint32_t n = w.last - w.first;
+        if (group * NK < n) ld.load(w.first + group * NK, list, n - group * NK, lds0);
+    }
     v4u q[DP / 16];
     load_q<DP>(p, w, q);
 
-    Reads<DP> rd(smem, TILE_B, w.half, w.col);
+    Reads<DP> rd(ring, TILE_B, w.half, w.col);
     Row<T, DP> r;
     r.clear();
     bool any = false;   // whether any key was allowed (the same for all rows)
@@ -511,44 +525,87 @@ __global__ __launch_bounds__(NW * 64, DP <= 64 && !MASK ? 4 : 2) void tile_kerne
     for (uint32_t from = w.first; from < w.last;) {
         uint32_t n = w.last - from;
         const uint32_t upto = MASK ? from + min(n, p.list_keys) : w.last;
-        if constexpr (MASK) n = list_keys<NW * 64>(mask, from, upto - from, list, counts);
+        if constexpr (MASK) n = list_keys<NW * KG * 64>(mask, from, upto - from, list, counts);
         any |= n != 0;
         const uint32_t tiles = (n + NK - 1) / NK;
-        auto load = [&](uint32_t t) {
-            const uint32_t lds = lds0 + (t & 1) * 2 * TILE_B;
-            ld.load(MASK ? from : from + t * NK, list + t * NK, n - t * NK, lds);
+        // tile t of the pass to buffer `to`, if there is one
+        auto load = [&](uint32_t t, uint32_t to) {
+            if (t < tiles)
+                ld.load(MASK ? from : from + t * NK, list + t * NK, n - t * NK, lds0 + to * 2 * TILE_B);
         };
-        if (MASK && tiles) load(0);
         if constexpr (MASK) {
+            load(group, 0);
             // one loop body, its places moved from buffer to buffer: with two
             // bodies in two nested loops the accumulators were held twice
             int other = 2 * TILE_B;
-            for (uint32_t t = 0; t < tiles; ++t) {
+            for (uint32_t i = 0, t = group; i < tiles; i += KG, t += KG) {
                 wait_vmcnt<0>();
                 workgroup_barrier();
-                if (t + 1 < tiles) load(t + 1);
-                r.template step<2, 0>(rd, q, n - t * NK, p.c, w.half);
+                load(t + KG, other > 0);
+                if (KG == 1 || t < tiles) r.template step<2, 0>(rd, q, n - t * NK, p.c, w.half);
                 rd.move(other);
                 other = -other;
             }
-            if (tiles & 1) rd.move(other);   // back to the first buffer
+            if (other < 0) rd.move(other);   // back to the first buffer
+            workgroup_barrier();             // the list and the buffers are free
         } else {
-            for (uint32_t t = 0; t < tiles; ++t) {
+            // i: the first group's tile, for an end that all groups share
+            for (uint32_t i = 0, t = group;; ) {
                 wait_vmcnt<0>();
                 workgroup_barrier();   // tile t is in LDS, and every wave is done with the other buffer
-                if (t + 1 < tiles) load(t + 1);
-                r.template step<2, 0>(rd, q, n - t * NK, p.c, w.half);
-                if (++t == tiles) break;
+                load(t + KG, 1);
+                if (KG == 1 || t < tiles) r.template step<2, 0>(rd, q, n - t * NK, p.c, w.half);
+                t += KG;
+                if ((i += KG) >= tiles) break;
                 wait_vmcnt<0>();
                 workgroup_barrier();
-                if (t + 1 < tiles) load(t + 1);
-                r.template step<2, 2 * TILE_B>(rd, q, n - t * NK, p.c, w.half);
+                load(t + KG, 0);
+                if (KG == 1 || t < tiles) r.template step<2, 2 * TILE_B>(rd, q, n - t * NK, p.c, w.half);
+                t += KG;
+                if ((i += KG) >= tiles) break;
             }
         }
-        if constexpr (MASK) workgroup_barrier();   // the list and the buffers are free
         from = upto;
     }
     r.finish(any);
+    if constexpr (KG > 1) {
+        // the same lane of every group holds the same row and channels
+        float* acc = reinterpret_cast<float*>(smem);
+        const uint32_t lane = threadIdx.x % (NW * 64);
+        __syncthreads();   // the rings are free
+        if (group > 0) {
+            ml[group - 1][lane] = make_float2(r.m, r.l);
+#pragma unroll
+            for (int b = 0; b < DB; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    acc[((group - 1) * DB * 16 + b * 16 + i) * (NW * 64) + lane] = r.o[b][i];
+        }
+        __syncthreads();
+        if (group > 0) return;
+        float m = r.m;
+#pragma unroll
+        for (int g = 0; g < KG - 1; ++g) m = fmaxf(m, ml[g][lane].x);
+        // (-inf) - (-inf) is no weight: such a group holds nothing
+        const float own = r.m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f((r.m - m) * p.c);
+        r.l *= own;
+#pragma unroll
+        for (int b = 0; b < DB; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r.o[b][i] *= own;
+#pragma unroll
+        for (int g = 0; g < KG - 1; ++g) {
+            const float2 t = ml[g][lane];
+            const float f = t.x == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f((t.x - m) * p.c);
+            r.l = __builtin_fmaf(t.y, f, r.l);
+#pragma unroll
+            for (int b = 0; b < DB; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    r.o[b][i] = __builtin_fmaf(acc[(g * DB * 16 + b * 16 + i) * (NW * 64) + lane], f, r.o[b][i]);
+        }
+        r.m = m;
+    }
     if (w.row >= p.rows) return;
     if (p.splits > 1) {
         const uint64_t at = ((uint64_t)w.bh * p.rows + w.row) * p.splits + w.split;
@@ -768,7 +825,7 @@ namespace {
 
 // How a call runs: by slices (few rows) or tiles, and over how many splits.
 struct Plan {
-    bool slices;
+    bool slices, two_groups;
     uint32_t m_tiles, splits, split_keys;
 };
 
@@ -777,21 +834,29 @@ constexpr int kTileWaves = 4;
 Plan plan_of(int64_t bh, int64_t rows, int64_t tk, int64_t d)
 {
     Plan p{};
-    p.slices = rows <= 96;
+    const int64_t cus = num_cus();
+    // Slices up to 96 rows, where most of a 128-row tile would idle, and up to
+    // 512 where 32-row workgroups still fill less than half of the chip (256
+    // rows, 8 heads of 128, 1024 keys: 11.3 us against 16.6; 256 rows, 64 heads
+    // of 128, where they do not: 27 against 22).
+    p.slices = rows <= 96 || (rows <= 512 && bh * ((rows + 31) / 32) < cus / 2);
     const int64_t tile_rows = p.slices ? 32 : 32 * kTileWaves;
     p.m_tiles = (uint32_t)((rows + tile_rows - 1) / tile_rows);
-    // As many splits as keep every workgroup resident at once (a slice workgroup
-    // of up to 64 channels takes under half of a CU's LDS): a second round of
-    // workgroups costs more than it balances, also where lengths differ.  A
-    // split below one slice a wave is not worth its join.
-    const int64_t groups = bh * p.m_tiles, cus = num_cus();
-    const int64_t resident = cus * (p.slices && d > 64 ? 1 : 2), least = p.slices ? 128 : 512;
+    // As many splits as keep every workgroup resident at once, one a CU (two
+    // slice workgroups of up to 64 channels share one): a second round of
+    // workgroups costs more than it balances, also where lengths differ.  The
+    // join costs about as much as 512 keys of a slice workgroup.
+    const int64_t groups = bh * p.m_tiles;
+    const int64_t resident = cus * (p.slices && d <= 64 ? 2 : 1), least = p.slices ? 128 : 512;
     int64_t splits = std::max<int64_t>(1, std::min(resident / groups, tk / least));
-    if (!p.slices && groups >= cus) splits = 1;
+    if (p.slices && tk < 768) splits = 1;
     const int64_t unit = 128;
     const int64_t keys = (tk + splits - 1) / splits;
     p.split_keys = (uint32_t)std::max<int64_t>(unit, (keys + unit - 1) / unit * unit);
     p.splits = (uint32_t)std::max<int64_t>(1, (tk + p.split_keys - 1) / p.split_keys);
+    // two groups of waves halve a workgroup's way through its keys, for about a
+    // microsecond to join them
+    p.two_groups = !p.slices && groups * p.splits <= cus && p.split_keys >= 512;
     return p;
 }
 
@@ -801,8 +866,10 @@ hipError_t launch(attn::Params& p, const Plan& plan, uint32_t bh, hipStream_t st
     const dim3 grid(bh * plan.m_tiles * plan.splits);
     if (plan.slices)
         attn::slice_kernel<T, DP, MASK><<<grid, dim3(256), 0, st>>>(p);
-    else
-        attn::tile_kernel<T, DP, kTileWaves, MASK><<<grid, dim3(kTileWaves * 64), 0, st>>>(p);
+    if (!plan.slices && plan.two_groups)
+        attn::tile_kernel<T, DP, kTileWaves, 2, MASK><<<grid, dim3(2 * kTileWaves * 64), 0, st>>>(p);
+    if (!plan.slices && !plan.two_groups)
+        attn::tile_kernel<T, DP, kTileWaves, 1, MASK><<<grid, dim3(kTileWaves * 64), 0, st>>>(p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || plan.splits == 1) return e;
     p.by_tiles = FastDiv(p.rows);
