@@ -58,7 +58,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libck_convrot.so")
@@ -159,13 +158,6 @@ def _call(name: str, *args) -> None:
 def _stream(t):
     import torch
     return torch.cuda.current_stream(t.device).cuda_stream
-
-
-def _raw_stream(dev):
-    """The current stream of device index `dev`, as _stream, without building a
-    Stream object (a microsecond less on calls of a few)."""
-    import torch
-    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _need(t, dtype, ndim, what):
@@ -678,124 +670,40 @@ def ck_swiglu_mlp_w8a16(x, w_gu, s_gu, w_down, s_down, group: int = 128, out=Non
 CK_DTYPE_BF16, CK_DTYPE_FP16 = 0, 1
 CK_PAIR_HALF, CK_PAIR_INTERLEAVED = 0, 1
 _PAIRING = {"half": CK_PAIR_HALF, "interleaved": CK_PAIR_INTERLEAVED}
-# ck_heads and ck_qk_side of include/ck.h as packed 8-byte words (bytes pass as
-# their address)
-_PACK_HEADS, _PACK_SIDE = struct.Struct("4Q"), struct.Struct("17Q")
+_calls = None
 
 
-def _heads(t, what, dtype, dev):
-    """Check a [batch, tokens, heads, d] tensor of 16-bit values; returns the
-    words of its ck_heads (address, batch, token and head strides).  dev: the
-    device index the call runs on (a CPU tensor's is -1)."""
-    if t.dtype is not dtype or t.get_device() != dev or t.dim() != 4:
-        raise ValueError(f"{what} needs a {dtype} [batch, tokens, heads, d] tensor on cuda:{dev}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
-    (b, n, h, d), (sb, sn, sh, sd) = t.shape, t.stride()
-    # the stride of a dimension of one element is never used
-    if b < 2:
-        sb = 0
-    if n < 2:
-        sn = 0
-    if h < 2:
-        sh = 0
-    p = t.data_ptr()
-    if sd != 1 or d < 8 or d & 7 or p & 15 or (sb | sn | sh) & 7:
-        raise ValueError(f"{what} needs contiguous heads of a multiple of 8 channels, 16-byte aligned (strides in "
-                         f"multiples of 8 elements), got shape {tuple(t.shape)}, strides {t.stride()}")
-    return p, sb, sn, sh
+def _native():
+    """The marshalling extension (csrc/marshal.cpp), bound to lib()'s functions."""
+    global _calls
+    if _calls is None:
+        import torch
+        L = lib()
+        try:
+            from . import _marshal as m
+        except ImportError as e:
+            raise ImportError(f"{os.path.join(HERE, '_marshal.so')} is missing or does not load ({e}): build it "
+                              "with `python -m swiglu_mlp_amd.build`") from e
+        m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                 for f in (L.ck_qk_norm_rope, L.ck_cross_attn, L.ck_cross_attn_workspace_size)),
+               torch._C._cuda_getCurrentRawStream)
+        _calls = m
+    return _calls
 
 
-def _first(t, what):
-    """The dtype code, dtype and device index that a call takes from its queries."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{what} must be a torch.Tensor on a GPU")
-    dtype = t.dtype
-    if dtype is torch.bfloat16:
-        return CK_DTYPE_BF16, dtype, t.get_device()
-    if dtype is torch.float16:
-        return CK_DTYPE_FP16, dtype, t.get_device()
-    raise ValueError(f"{what} needs dtype bfloat16 or float16, got {dtype}")
+def _done(name, r):
+    """A marshalled call's result, or CKError for a C status."""
+    if r.__class__ is int:
+        raise CKError(name, r, lib().ck_status_str(r).decode())
+    return r
 
 
-def _view_span(t):
-    """Byte range [a, b) that a strided tensor lies in."""
-    n = sum((s - 1) * st for s, st in zip(t.shape, t.stride())) + 1 if t.numel() else 0
-    return t.data_ptr(), t.data_ptr() + n * t.element_size()
-
-
-def _disjoint(a, b):
-    """Whether two [batch, tokens, heads, d] views share no element: apart in
-    memory, or different column ranges of rows with the same pitch."""
-    (a0, a1), (b0, b1) = _view_span(a), _view_span(b)
-    if a1 <= b0 or b1 <= a0:
-        return True
-    pitch = a.stride(1)
-    if a.shape[1] < 2 or b.shape[1] < 2 or b.stride(1) != pitch:
-        return False
-    for t in (a, b):   # one pitch over all (batch, token) rows
-        if t.shape[0] > 1 and t.stride(0) % pitch:
-            return False
-    w = [(t.shape[2] - 1) * t.stride(2) + t.shape[3] for t in (a, b)]
-    gap = (b0 - a0) // a.element_size() % pitch    # b's columns start `gap` after a's
-    return w[0] <= gap and gap + w[1] <= pitch
-
-
-def _heads_out(out, like, words, what, others, in_place, dtype, dev):
-    """An output shaped like the queries or keys `like` (whose ck_heads words
-    are `words`), and its own words: a new contiguous tensor, or `out` checked.
-    `out` shares no element with `like` and the `others`, or it is `like` itself
-    where `in_place` allows that (each head is read before it is written)."""
-    if out is None:
-        out = like.new_empty(like.shape)
-        _, n, h, d = like.shape
-        return out, (out.data_ptr(), n * h * d, h * d, d)
-    at = _heads(out, what, dtype, dev)
-    if out.shape != like.shape:
-        raise ValueError(f"{what} needs shape {tuple(like.shape)}, got {tuple(out.shape)}")
-    if any(n > 1 and st == 0 for n, st in zip(out.shape, out.stride())):
-        raise ValueError(f"{what} must not be an expanded tensor")
-    if not in_place or at != words:
-        others = (like, *others)
-    if not all(_disjoint(out, t) for t in others):
-        raise ValueError(f"{what} must not share memory with what the call reads")
-    return out, at
-
-
-def _rope(rope, half, what, dev):
-    """(cos address, sin address, rows) of a side's rotation tables."""
-    import torch
-    cos, sin = rope
-    shape = cos.shape
-    if (cos.dtype is not torch.float32 or sin.dtype is not torch.float32 or len(shape) != 2 or shape[1] != half
-            or sin.shape != shape or cos.get_device() != dev or sin.get_device() != dev
-            or not cos.is_contiguous() or not sin.is_contiguous()):
-        raise ValueError(f"{what}_rope needs contiguous float32 [rows, {half}] cos and sin of one shape on cuda:{dev}")
-    return cos.data_ptr(), sin.data_ptr(), shape[0]
-
-
-def _qk_side(words, sizes, out_words, weight, rope, pos, d, what, dev):
-    """One side's ck_qk_side (include/ck.h), packed; rope: from _rope, or None."""
-    import torch
-    b, n, h = sizes
-    w = cos = sin = rows = pos_p = pos_st = 0
-    if weight is not None:
-        if (weight.dtype is not torch.float32 or weight.shape != (d,) or weight.get_device() != dev
-                or not weight.is_contiguous()):
-            raise ValueError(f"{what}_weight needs a contiguous float32 ({d},) tensor on cuda:{dev}")
-        w = weight.data_ptr()
-    if rope is not None:
-        cos, sin, rows = rope
-        if pos is not None:
-            if (pos.dtype is not torch.int32 or pos.shape != (b, n) or pos.get_device() != dev
-                    or (n > 1 and pos.stride(1) != 1)):
-                raise ValueError(f"{what}_pos needs an int32 ({b}, {n}) tensor with contiguous rows on cuda:{dev}")
-            pos_p, pos_st = pos.data_ptr(), pos.stride(0) if b > 1 else 0
-        elif n > rows:
-            raise ValueError(f"{what}_rope has {rows} rows for {n} tokens")
-    elif pos is not None:
-        raise ValueError(f"{what}_pos without {what}_rope")
-    return _PACK_SIDE.pack(*words, *out_words, b, n, h, w, cos, sin, rows, pos_p, pos_st)
+def _cos_sin(rope):
+    if rope is None:
+        return None, None
+    if not isinstance(rope, (tuple, list)) or len(rope) != 2:
+        raise ValueError("a rope is (cos, sin)")
+    return rope
 
 
 def ck_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, q_rope=None, k_rope=None, q_pos=None,
@@ -812,42 +720,9 @@ def ck_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, q_rope=None, k_rope
     themselves.  Returns q_out, or (q_out, k_out) when k is given."""
     if pairing not in _PAIRING:
         raise ValueError(f"unknown pairing {pairing!r}")
-    code, dtype, dev = _first(q, "q")
-    hq = _heads(q, "q", dtype, dev)
-    *q_sizes, d = q.shape
-    if d > 256:
-        raise ValueError(f"head size {d} is over 256")
-    half = 0
-    tq = tk = None
-    first = q_rope if q_rope is not None else k_rope
-    if first is not None:
-        for rope in (q_rope, k_rope):
-            if rope is not None and (not isinstance(rope, (tuple, list)) or len(rope) != 2):
-                raise ValueError("a rope is (cos, sin)")
-        half = first[0].shape[-1]
-        if 2 * half > d or half % (8 if pairing == "half" else 4):
-            raise ValueError(f"the rotated channels must be a multiple of {16 if pairing == 'half' else 8} up to {d}, "
-                             f"got {2 * half}")
-        if q_rope is not None:
-            tq = _rope(q_rope, half, "q", dev)
-        if k_rope is not None:
-            tk = tq if k_rope is q_rope else _rope(k_rope, half, "k", dev)
-    y, hy = _heads_out(q_out, q, hq, "q_out", () if k is None else (k,), True, dtype, dev)
-    side_q = _qk_side(hq, q_sizes, hy, q_weight, tq, q_pos, d, "q", dev)
-    z = side_k = None
-    if k is not None:
-        hk = _heads(k, "k", dtype, dev)
-        *k_sizes, dk = k.shape
-        if dk != d:
-            raise ValueError(f"q and k need one head size, got {d} and {dk}")
-        z, hz = _heads_out(k_out, k, hk, "k_out", (q,), True, dtype, dev)
-        if q_out is not None and k_out is not None and not _disjoint(y, z):
-            raise ValueError("q_out and k_out must not share memory")
-        side_k = _qk_side(hk, k_sizes, hz, k_weight, tk, k_pos, d, "k", dev)
-    elif k_weight is not None or k_rope is not None or k_pos is not None or k_out is not None:
-        raise ValueError("arguments for k without k")
-    _call("ck_qk_norm_rope", side_q, side_k, d, 2 * half, _PAIRING[pairing], code, eps, _raw_stream(dev))
-    return y if k is None else (y, z)
+    return _done("ck_qk_norm_rope", (_calls or _native()).qk_norm_rope(
+        q, k, q_weight, k_weight, *_cos_sin(q_rope), *_cos_sin(k_rope), q_pos, k_pos, _PAIRING[pairing], eps,
+        q_out, k_out))
 
 
 def ck_cross_attn(q, k, v, scale=None, kv_len=None, key_mask=None, out=None, workspace=None):
@@ -860,45 +735,7 @@ def ck_cross_attn(q, k, v, scale=None, kv_len=None, key_mask=None, out=None, wor
     key_mask bool or uint8 [kv_batch, tk]: False / 0 keys are left out.  What is
     left out is not read; a row with no key is zero.
     Returns [batch, tq, heads, d], contiguous unless `out` is given."""
-    import torch
-    code, dtype, dev = _first(q, "q")
-    hq, hk, hv = _heads(q, "q", dtype, dev), _heads(k, "k", dtype, dev), _heads(v, "v", dtype, dev)
-    b, tq, h, d = q.shape
-    kb, tk, kh, dk = k.shape
-    if v.shape != k.shape:
-        raise ValueError(f"k and v need one shape, got {tuple(k.shape)} and {tuple(v.shape)}")
-    if dk != d or d > 128:
-        raise ValueError(f"q and k need one head size up to 128, got {d} and {dk}")
-    if b and tq and h and (not kb or b % kb or not kh or h % kh):
-        raise ValueError(f"batch {b} and heads {h} must be multiples of the encoder's {kb} and {kh}")
-    scale = d ** -0.5 if scale is None else float(scale)
-    if not 0.0 < scale < 3.4e38:
-        raise ValueError(f"scale must be positive and finite, got {scale}")
-    len_p = mask_p = ws_p = None
-    mask_st = ws_n = 0
-    if kv_len is not None:
-        if (kv_len.dtype is not torch.int32 or kv_len.shape != (kb,) or kv_len.get_device() != dev
-                or not kv_len.is_contiguous()):
-            raise ValueError(f"kv_len needs a contiguous int32 ({kb},) tensor on cuda:{dev}")
-        len_p = kv_len.data_ptr()
-    if key_mask is not None:
-        if (key_mask.dtype not in (torch.bool, torch.uint8) or key_mask.shape != (kb, tk)
-                or key_mask.get_device() != dev or (tk > 1 and key_mask.stride(1) != 1)):
-            raise ValueError(f"key_mask needs a bool or uint8 ({kb}, {tk}) tensor with contiguous rows on cuda:{dev}")
-        mask_p, mask_st = key_mask.data_ptr(), key_mask.stride(0) if kb > 1 else 0
-    y, hy = _heads_out(out, q, hq, "out", (k, v), False, dtype, dev)
-    need = lib().ck_cross_attn_workspace_size(b, kb, tq, tk, h, kh, d)
-    if need:
-        if workspace is None:
-            workspace = q.new_empty((need // 2,))
-            ws_n = need
-        else:
-            ws_n = _workspace(workspace, need, q.device).numel()
-        ws_p = workspace.data_ptr()
-    pack = _PACK_HEADS.pack
-    _call("ck_cross_attn", pack(*hq), pack(*hk), pack(*hv), pack(*hy), b, kb, tq, tk, h, kh, d, code, scale,
-          len_p, mask_p, mask_st, ws_p, ws_n, _raw_stream(dev))
-    return y
+    return _done("ck_cross_attn", (_calls or _native()).cross_attn(q, k, v, scale, kv_len, key_mask, out, workspace))
 
 
 def ck_silu_f32(gate):

@@ -1,4 +1,5 @@
-"""Build the gfx950 HIP library ``swiglu_mlp_amd/libck_convrot.so`` in-tree.
+"""Build the gfx950 HIP library ``swiglu_mlp_amd/libck_convrot.so`` and the
+Python extension ``swiglu_mlp_amd/_marshal.so`` in-tree.
 
 Every translation unit is compiled by hipcc for gfx950 only, with
 ``-ffp-contract=off`` (the quantizer's FP32 steps must not be fused) and with
@@ -11,14 +12,17 @@ import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libck_convrot.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 SOURCES = ["api.hip", "quant.hip", "gemm.hip", "gemm_big.hip", "gemm_blk.hip", "gemm_small.hip",
-           "gemm_fused.hip", "qknorm.hip", "attn.hip", "probe.hip"]
+           "gemm_fused.hip", "qknorm.hip", "attn.hip", "attn_bf16.hip",
+           "attn_fp16.hip", "probe.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -46,11 +50,30 @@ def _compile(src: str, obj_dir: str, report: bool) -> str:
     return obj
 
 
+def _marshal() -> None:
+    """The argument marshalling extension (host code, g++, torch's headers)."""
+    import torch
+    home = os.path.dirname(torch.__file__)
+    tmp = MARSHAL + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-I{INCLUDE}", "-isystem", os.path.join(home, "include"),
+           "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "marshal.cpp"), "-o", tmp,
+           "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed on marshal.cpp:\n" + r.stdout + r.stderr)
+    os.replace(tmp, MARSHAL)
+
+
 def build(report: bool = False) -> str:
     obj_dir = os.path.join(ROOT, "_build", "ck")
     os.makedirs(obj_dir, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        marshal = ex.submit(_marshal)
         objs = list(ex.map(lambda s: _compile(s, obj_dir, report), SOURCES))
+        marshal.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     r = subprocess.run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp],
                        capture_output=True, text=True)
