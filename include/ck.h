@@ -389,7 +389,7 @@ typedef struct ck_qk_side {
  * pos, tokens <= table_rows.
  * Errors: CK_EINVAL on null or misaligned pointers, unknown type or pairing,
  * eps; CK_ESHAPE on sizes and strides; CK_EUNSUPPORTED on d > 256 or a side of
- * 2^31 or more heads. */
+ * 2^25 or more heads (batch * tokens * heads). */
 ck_status ck_qk_norm_rope(const ck_qk_side *q, const ck_qk_side *k, int64_t d, int64_t rot,
                           int32_t pairing, int32_t dtype, float eps, void *stream);
 
@@ -415,8 +415,9 @@ ck_status ck_qk_norm_rope(const ck_qk_side *q, const ck_qk_side *k, int64_t d, i
  *   workspace  ck_cross_attn_workspace_size(...) bytes (0: may be NULL),
  *              256-byte aligned, clobbered
  * Errors: CK_EINVAL on null or misaligned pointers, unknown type, scale;
- * CK_ESHAPE on sizes and strides; CK_EUNSUPPORTED on d > 128 or 2^31 or more
- * rows or key heads; CK_EWORKSPACE. */
+ * CK_ESHAPE on sizes and strides; CK_EUNSUPPORTED on d > 128, on 2^30 or more
+ * rows (batch * tq * heads) or 2^22 or more key heads (kv_batch * kv_heads);
+ * CK_EWORKSPACE. */
 ck_status ck_cross_attn(const ck_heads *q, const ck_heads *k, const ck_heads *v, const ck_heads *o,
                         int64_t batch, int64_t kv_batch, int64_t tq, int64_t tk, int64_t heads,
                         int64_t kv_heads, int64_t d, int32_t dtype, float scale,

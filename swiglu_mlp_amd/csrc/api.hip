@@ -116,9 +116,9 @@ const char* ck_status_str(ck_status s)
 {
     switch (s) {
         case CK_OK: return "ok";
-        case CK_EINVAL: return "invalid argument (null or misaligned pointer, unknown act)";
-        case CK_ESHAPE: return "bad shape (negative size, k % group, k % 64, n % 16, leading dimension)";
-        case CK_EUNSUPPORTED: return "unsupported (group not a power of two <= 256, k > CK_MAX_K, a buffer past 2^31 bytes, or the decode layout with m > 64)";
+        case CK_EINVAL: return "invalid argument (null or misaligned pointer, unknown act or type, eps or scale out of range)";
+        case CK_ESHAPE: return "bad shape (negative size, k % group, k % 64, n % 16, leading dimension; head size, strides, batch or head counts)";
+        case CK_EUNSUPPORTED: return "unsupported (group not a power of two <= 256, k > CK_MAX_K, a buffer past 2^31 bytes, the decode layout with m > 64, or a head size or count past its limit)";
         case CK_EWORKSPACE: return "workspace missing or too small";
         case CK_EHIP: return "HIP runtime error at launch";
     }
@@ -587,14 +587,18 @@ static int64_t product_below(int64_t a, int64_t b, int64_t c, int64_t limit)
     return a * b * c < limit ? a * b * c : limit;
 }
 
-constexpr int64_t kMaxRows = 0x7fffffffLL;
+// Sizes whose launches stay below 2^32 threads in a grid.
+constexpr int64_t kMaxIndex = 0x7fffffffLL;   // a dimension alone
+constexpr int64_t kMaxNormHeads = 1 << 25;    // batch * tokens * heads of a side of the norm (32 lanes each)
+constexpr int64_t kMaxAttnRows = 1 << 30;     // batch * tq * heads
+constexpr int64_t kMaxKeyHeads = 1 << 22;     // kv_batch * kv_heads
 
 static ck_status check_qk_side(const ck_qk_side& s, int64_t rot, ck::QkSideArgs* out)
 {
     *out = ck::QkSideArgs{};
     if (s.batch < 0 || s.tokens < 0 || s.heads < 0) return CK_ESHAPE;
-    const int64_t rows = product_below(s.batch, s.tokens, s.heads, kMaxRows);
-    if (rows >= kMaxRows) return CK_EUNSUPPORTED;
+    const int64_t rows = product_below(s.batch, s.tokens, s.heads, kMaxNormHeads);
+    if (rows >= kMaxNormHeads) return CK_EUNSUPPORTED;
     if (rows == 0) return CK_OK;
     CK_TRY(check_heads(s.x));
     CK_TRY(check_heads(s.y));
@@ -602,7 +606,7 @@ static ck_status check_qk_side(const ck_qk_side& s, int64_t rot, ck::QkSideArgs*
     const bool rope = rot > 0 && (s.cos || s.sin);
     if (rope) {
         if (!s.cos || !s.sin || !aligned16(s.cos) || !aligned16(s.sin)) return CK_EINVAL;
-        if (s.table_rows < 1 || s.table_rows > kMaxRows) return CK_ESHAPE;
+        if (s.table_rows < 1 || s.table_rows > kMaxIndex) return CK_ESHAPE;
         if (s.pos ? s.pos_stride < 0 : s.tokens > s.table_rows) return CK_ESHAPE;
         if (s.pos && ((uintptr_t)s.pos & 3u)) return CK_EINVAL;
     }
@@ -645,7 +649,9 @@ static ck_status check_attn_sizes(int64_t batch, int64_t kv_batch, int64_t tq, i
     if (d > 128) return CK_EUNSUPPORTED;
     if (batch == 0 || tq == 0 || heads == 0) return CK_OK;
     if (kv_batch == 0 || batch % kv_batch != 0 || kv_heads == 0 || heads % kv_heads != 0) return CK_ESHAPE;
-    if (tk > kMaxRows || product_below(batch, tq, heads, kMaxRows) >= kMaxRows) return CK_EUNSUPPORTED;
+    if (tk > kMaxIndex || product_below(batch, tq, heads, kMaxAttnRows) >= kMaxAttnRows ||
+        product_below(kv_batch, kv_heads, 1, kMaxKeyHeads) >= kMaxKeyHeads)
+        return CK_EUNSUPPORTED;
     return CK_OK;
 }
 

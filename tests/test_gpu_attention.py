@@ -445,3 +445,21 @@ def test_refusals():
     if need:
         z = torch.zeros(1, 100_000, 1, 64, dtype=BF16, device=DEV)
         no(c, z[:, :1], z, z, workspace=torch.empty(need - 1, dtype=torch.uint8, device=DEV))
+
+
+# ---------------------------------------------------------------- the block of both
+def test_block_of_linears_norms_and_attention():
+    """The example block against FP32 with unquantized weights.  Its INT8 linears are of the 1 to 2% class (relative
+    L2); four in a row, with residuals that are not quantized, stay under 5%."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    from examples import cross_block as cb
+    weights, x, context, rope, lens = cb.synthetic(b=3, t=50, s=33, heads=4, d=64, context=256, inner=512)
+    lens[0] = 0                                    # a prompt without states: attention adds nothing
+    y = cb.CrossBlock(weights, 4)(x, context, rope, lens).float()
+    one = lens.clone().clamp(min=1)                # (the reference has no empty softmax)
+    want = cb.reference(weights, 4, x, context, rope, one)
+    want[0] = cb.reference({**weights, "w_o": 0 * weights["w_o"]}, 4, x[:1], context[:1], rope, one[:1])[0]
+    for i in range(3):
+        assert ((y[i] - want[i]).norm() / want[i].norm()).item() < 0.05
