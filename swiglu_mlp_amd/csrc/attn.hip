@@ -69,7 +69,9 @@ hipError_t launch_cross_attn(const AttnArgs& a, hipStream_t st)
     p.by_tq = FastDiv((uint32_t)a.tq);
     p.by_hkv = FastDiv((uint32_t)a.kv_heads);
     const int64_t bh = a.kv_batch * a.kv_heads;
-    const attn::Plan plan = plan_of(bh, p.rows, a.tk, a.d);
+    attn::Plan plan = plan_of(bh, p.rows, a.tk, a.d);
+    // with lengths, whose values only the device knows, half of the keys
+    plan.streamed = plan.m_tiles == 1 && bh * a.tk * a.d * 4 / (a.kv_len ? 2 : 1) >= kInfinityCacheBytes;
     p.m_tiles = plan.m_tiles;
     p.splits = plan.splits;
     p.split_keys = plan.split_keys;

@@ -29,10 +29,10 @@ struct Params {
     FastDiv by_g, by_tq, by_hkv, by_tiles, by_splits;
 };
 
-// How a call runs: by slices (few rows) or tiles, with one or two key groups a
-// workgroup, and over how many splits.
+// How a call runs: by slices (few rows; their keys streamed past the caches or
+// not) or tiles, with one or two key groups a workgroup, and over how many splits.
 struct Plan {
-    bool slices, two_groups;
+    bool slices, streamed, two_groups;
     uint32_t m_tiles, splits, split_keys;
 };
 

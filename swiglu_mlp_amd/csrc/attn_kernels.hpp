@@ -75,16 +75,27 @@ __device__ __forceinline__ void workgroup_barrier()
 
 // 16 bytes per lane from a buffer to LDS: lane l's land at byte lds + 16 l.
 // Inline assembly, so that the compiler does not wait for it before unrelated
-// LDS reads; the caller waits (wait_vmcnt) before the data's first use.
+// LDS reads; the caller waits (wait_vmcnt) before the data's first use.  NT:
+// nontemporal.
+template <bool NT>
 __device__ __forceinline__ void lds_dma_b128(v4i rsrc, uint32_t voff, uint32_t lds)
 {
-    asm volatile(
-        "s_mov_b32 m0, %2\n\t"
-        "s_nop 0\n\t"
-        "buffer_load_dwordx4 %0, %1, 0 offen lds"
-        :
-        : "v"(voff), "s"(rsrc), "s"(lds)
-        : "memory");
+    if constexpr (NT)
+        asm volatile(
+            "s_mov_b32 m0, %2\n\t"
+            "s_nop 0\n\t"
+            "buffer_load_dwordx4 %0, %1, 0 offen nt lds"
+            :
+            : "v"(voff), "s"(rsrc), "s"(lds)
+            : "memory");
+    else
+        asm volatile(
+            "s_mov_b32 m0, %2\n\t"
+            "s_nop 0\n\t"
+            "buffer_load_dwordx4 %0, %1, 0 offen lds"
+            :
+            : "v"(voff), "s"(rsrc), "s"(lds)
+            : "memory");
 }
 
 __device__ __forceinline__ v4i make_rsrc(const void* base)
@@ -238,7 +249,7 @@ __device__ uint32_t list_keys(const uint8_t* mask, uint32_t from, uint32_t n, ui
 // A wave's loads of a K or V tile of NK keys into LDS: CNT of its NK DP / 512
 // one-KB pieces, from piece `first` on, a 16-byte chunk per lane.  LISTED: the
 // keys come through a list of their indices.
-template <int DP, int NK, int CNT, bool LISTED>
+template <int DP, int NK, int CNT, bool LISTED, bool NT>
 struct Loader {
     static constexpr int CH = DP / 8;
     const char* base;      // key 0 of the head
@@ -279,7 +290,7 @@ struct Loader {
         const v4i rsrc = make_rsrc(base + (uint64_t)key * pitch);
         if (!LISTED && left >= (uint32_t)NK) {
 #pragma unroll
-            for (int i = 0; i < CNT; ++i) lds_dma_b128(rsrc, off[i], lds + (first + i) * 1024);
+            for (int i = 0; i < CNT; ++i) lds_dma_b128<NT>(rsrc, off[i], lds + (first + i) * 1024);
         } else {
             uint32_t at[CNT];
 #pragma unroll
@@ -290,7 +301,7 @@ struct Loader {
                 if (past(i, left)) at[i] = kBufferOutside;
             }
 #pragma unroll
-            for (int i = 0; i < CNT; ++i) lds_dma_b128(rsrc, at[i], lds + (first + i) * 1024);
+            for (int i = 0; i < CNT; ++i) lds_dma_b128<NT>(rsrc, at[i], lds + (first + i) * 1024);
         }
     }
 };
@@ -482,7 +493,7 @@ __global__ __launch_bounds__(NW * KG * 64, DP <= 64 && KG == 1 && !MASK ? 4 : 2)
     const uint32_t group = all_wave / NW;
     const int wave = all_wave % NW;
     const Place w = place_of(p, wave * 32, NW * 32);
-    Loader<DP, NK, CNT, MASK> ld;
+    Loader<DP, NK, CNT, MASK, false> ld;
     ld.init(p, w, wave >= NW / 2, wave % (NW / 2) * CNT);
     const char* ring = smem + group * RING_B;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem + group * RING_B +
@@ -620,8 +631,11 @@ __global__ __launch_bounds__(NW * KG * 64, DP <= 64 && KG == 1 && !MASK ? 4 : 2)
 }
 
 // Few rows: 4 waves on the same 32 rows, each streaming every fourth slice of
-// 32 keys through two buffers of its own.
-template <typename T, int DP, bool MASK>
+// 32 keys through two buffers of its own.  NT: nontemporal loads of K and V, for
+// calls that read them once and past the Infinity Cache (one token over 131072
+// keys, 8 key heads of 128, 537 MB: 89 us, 99 without; over 67 MB of keys 17.2,
+// 16.6 without).
+template <typename T, int DP, bool MASK, bool NT>
 __global__ __launch_bounds__(256, 1) void slice_kernel(Params p)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -640,7 +654,7 @@ __global__ __launch_bounds__(256, 1) void slice_kernel(Params p)
     const Place w = place_of(p, 0, 32);
     v4u q[DP / 16];
     load_q<DP>(p, w, q);
-    Loader<DP, NK, CNT, MASK> lk, lv;
+    Loader<DP, NK, CNT, MASK, NT> lk, lv;
     lk.init(p, w, false, 0);
     lv.init(p, w, true, 0);
     const Reads<DP> rd(smem + wave * (2 * 2 * SLICE_B), SLICE_B, w.half, w.col);
@@ -801,8 +815,10 @@ template <typename T, int DP, bool MASK>
 hipError_t launch_padded(Params& p, const Plan& plan, uint32_t bh, hipStream_t st)
 {
     const dim3 grid(bh * plan.m_tiles * plan.splits);
-    if (plan.slices)
-        slice_kernel<T, DP, MASK><<<grid, dim3(256), 0, st>>>(p);
+    if (plan.slices && plan.streamed)
+        slice_kernel<T, DP, MASK, true><<<grid, dim3(256), 0, st>>>(p);
+    if (plan.slices && !plan.streamed)
+        slice_kernel<T, DP, MASK, false><<<grid, dim3(256), 0, st>>>(p);
     if (!plan.slices && plan.two_groups)
         tile_kernel<T, DP, kTileWaves, 2, MASK><<<grid, dim3(2 * kTileWaves * 64), 0, st>>>(p);
     if (!plan.slices && !plan.two_groups)

@@ -9,6 +9,12 @@ typedef __bf16 bf16;
 typedef _Float16 f16;
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 
+// What the Infinity Cache behind the XCDs' L2s holds.  A stream of more than
+// that finds nothing of itself there on the next call, and loads and stores
+// marked nontemporal (not kept) run faster; a smaller one does find it, and they
+// run slower.
+constexpr int64_t kInfinityCacheBytes = 256 << 20;
+
 // n / d for n < 2^31 and 1 <= d < 2^31 as one high product and a shift, after
 // Granlund and Montgomery, "Division by invariant integers using
 // multiplication" (1994): with s = ceil(log2 d) - 1 and m = floor(2^(32+s) / d)

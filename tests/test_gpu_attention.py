@@ -159,6 +159,17 @@ def test_norm_strides_zeros_and_extremes():
     check_norm(ck.ck_qk_norm_rope(b), b, None, None, None, "half", 1e-6)
 
 
+@pytest.mark.parametrize("pairing,dtype", [("half", BF16), ("interleaved", FP16)])
+def test_norm_past_the_caches(pairing, dtype):
+    # over 256 MiB read and written: the nontemporal form
+    g = gen(12)
+    qkv = torch.randn(1, 13_500, 40, 128, generator=g, device=DEV).to(dtype)
+    rope = tables(13_500, 128, g)
+    y, z = ck.ck_qk_norm_rope(qkv[:, :, :35], qkv[:, :, 35:], q_rope=rope, k_rope=rope, pairing=pairing)
+    check_norm(y, qkv[:, :, :35], None, rope, None, pairing, 1e-6)
+    check_norm(z, qkv[:, :, 35:], None, rope, None, pairing, 1e-6)
+
+
 def test_norm_empty():
     q = torch.empty(2, 0, 4, 64, dtype=BF16, device=DEV)
     k = torch.randn(2, 3, 4, 64, device=DEV).to(BF16)
@@ -317,6 +328,16 @@ def test_attn_growing_scores(tq, dtype):
     k = (torch.arange(700, device=DEV)[None, :, None, None] / 60.0 * torch.ones_like(k) + 0.1 * k.float()).to(dtype)
     check_attn(ck.ck_cross_attn(q, k, v), q, k, v)
     check_attn(ck.ck_cross_attn(q, k.flip(1).contiguous(), v), q, k.flip(1), v)
+
+
+@pytest.mark.parametrize("dtype,d,tk", [(BF16, 128, 70_000), (FP16, 64, 131_072), (BF16, 80, 120_001)])
+def test_attn_past_the_caches(dtype, d, tk):
+    # over 256 MiB of keys and values for one row tile: the streamed form
+    q, k, v = make(1, 3, 1, tk, 16, 8, d, dtype)
+    check_attn(ck.ck_cross_attn(q, k, v), q, k, v)
+    q, k, v = make(2, 1, 1, tk, 16, 8, d, dtype)
+    lens = torch.tensor([tk - 77, 333], dtype=torch.int32, device=DEV)
+    check_attn(ck.ck_cross_attn(q, k, v, kv_len=lens), q, k, v, kv_len=lens)
 
 
 @pytest.mark.parametrize("scale", [1e-3, 0.5, 2.0])
