@@ -62,6 +62,7 @@ hipError_t launch_cross_attn(const AttnArgs& a, hipStream_t st)
     p.d = (uint32_t)a.d;
     p.share = (uint32_t)(a.batch / a.kv_batch);
     p.heads_kv = (uint32_t)a.kv_heads;
+    p.kv_batch = (uint32_t)a.kv_batch;
     const int64_t g = a.heads / a.kv_heads;
     p.rows = (uint32_t)(p.share * a.tq * g);
     p.c = a.scale * 1.44269504088896340736f;

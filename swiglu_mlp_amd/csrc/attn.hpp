@@ -20,7 +20,7 @@ struct Params {
     const int32_t* kv_len;
     const uint8_t* mask;
     int64_t mask_sb;
-    uint32_t tk, d, share, heads_kv, rows, m_tiles;
+    uint32_t tk, d, share, kv_batch, heads_kv, rows, m_tiles;
     uint32_t splits, split_keys;    // keys [split_keys s, split_keys (s + 1)) belong to split s
     uint32_t list_keys;             // keys listed at a time: at most kList, their offsets in 32 bits
     float c;                        // scale * log2(e)

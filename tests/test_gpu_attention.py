@@ -288,6 +288,16 @@ def test_attn_lengths_and_masks(kb, share, tq, tk, h, kh, d, dtype):
     check_attn(ck.ck_cross_attn(q, k, v, key_mask=none), q, k, v, key_mask=none)
 
 
+@pytest.mark.parametrize("kb", [2, 15, 16, 17, 70])
+@pytest.mark.parametrize("tq", [1, 130])
+def test_attn_lengths_in_any_order(kb, tq):
+    # the longest sequences are taken first, up to 16 of them; equal lengths, none and all among them
+    q, k, v = make(kb, 1, tq, 100, 2, 2, 64, BF16)
+    lens = torch.randint(-3, 104, (kb,), generator=gen(13), device=DEV, dtype=torch.int32)
+    lens[: kb // 3] = 50
+    check_attn(ck.ck_cross_attn(q, k, v, kv_len=lens), q, k, v, kv_len=lens)
+
+
 @pytest.mark.parametrize("tq,share", [(1, 1), (1, 3), (50, 1), (300, 1)])
 def test_attn_nan_and_inf_in_masked_places(tq, share):
     q, k, v = make(2, share, tq, 400, 4, 2, 128, BF16)
