@@ -12,17 +12,22 @@ attn::Plan plan_of(int64_t bh, int64_t rows, int64_t tk, int64_t d)
 {
     attn::Plan p{};
     const int64_t cus = num_cus();
-    // Slices up to 96 rows, where most of a 128-row tile would idle, and up to
-    // 512 where 32-row workgroups still fill less than half of the chip (256
-    // rows, 8 heads of 128, 1024 keys: 11.3 us against 16.6; 256 rows, 64 heads
-    // of 128, where they do not: 27 against 22).
+    // Slices up to 96 rows, where part of a 128-row tile would idle (96 rows, 16
+    // heads of 128, 2048 keys: 13.9 us, tiles 17.5; 64 rows, 64 heads of 128, 1024
+    // keys: 15.2 and 17.4; 64 rows, 64 heads of 64, 4096 keys: 19.2 and 19.0), and
+    // up to 512 where 32-row workgroups fill less than half of the chip (256 rows,
+    // 8 heads of 128, 1024 keys: 11.3 and 16.6; but 128 rows, 64 heads of 64, 4096
+    // keys: 26.8 and 22.2).
     p.slices = rows <= 96 || (rows <= 512 && bh * ((rows + 31) / 32) < cus / 2);
     const int64_t tile_rows = p.slices ? 32 : 32 * attn::kTileWaves;
     p.m_tiles = (uint32_t)((rows + tile_rows - 1) / tile_rows);
     // As many splits as keep every workgroup resident at once, one a CU (two
     // slice workgroups of up to 64 channels share one): a second round of
-    // workgroups costs more than it balances, also where lengths differ.  The
-    // join costs about as much as 512 keys of a slice workgroup.
+    // workgroups costs more than it balances, also where lengths differ (one token,
+    // 8 sequences of 2048 keys, 8 heads of 128: 4 splits 16.6 us, 8 splits 20).
+    // The join costs about as much as 512 keys of a slice workgroup (128 rows, 16
+    // heads of 128, 512 keys: one split 8.6 us, two 10.4; one token, 8 heads, 512
+    // keys: 7.4 and, with four, 7.2, but a second launch).
     const int64_t groups = bh * p.m_tiles;
     const int64_t resident = cus * (p.slices && d <= 64 ? 2 : 1), least = p.slices ? 128 : 512;
     int64_t splits = std::max<int64_t>(1, std::min(resident / groups, tk / least));
@@ -32,7 +37,8 @@ attn::Plan plan_of(int64_t bh, int64_t rows, int64_t tk, int64_t d)
     p.split_keys = (uint32_t)std::max<int64_t>(unit, (keys + unit - 1) / unit * unit);
     p.splits = (uint32_t)std::max<int64_t>(1, (tk + p.split_keys - 1) / p.split_keys);
     // two groups of waves halve a workgroup's way through its keys, for about a
-    // microsecond to join them
+    // microsecond to join them (1000 rows, 8 heads of 128, 8192 keys: 46.0 us, one
+    // group 49.4; 1024 rows, 32 heads of 96, 128 keys: 8.4 and 7.1)
     p.two_groups = !p.slices && groups * p.splits <= cus && p.split_keys >= 512;
     return p;
 }

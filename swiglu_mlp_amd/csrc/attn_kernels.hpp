@@ -33,11 +33,16 @@
 // zeros, and their scores are set to -inf.
 //
 // Two kernels.  tile_kernel: the waves of a workgroup hold different rows and
-// share each K / V tile (many rows: bound by the matrix cores).  slice_kernel:
-// the waves hold the same 32 rows and each streams its own 32-key slices
-// through LDS of its own, without a barrier (few rows: bound by HBM).  Either
-// may split the keys over several workgroups; the unnormalised FP32 partial
-// results then go to the workspace and join_kernel adds them in a fixed order.
+// share each K / V tile.  Many rows are bound by the matrix cores, and those by
+// the chip's power: 24 heads of 128, 16384 rows over 4096 keys take 742 us (1110
+// TFLOP/s, a plain BF16 library product 1263) at 1.5 GHz with the matrix cores
+// busy 58% of the time; on zeros, 548.  A tile costs a wave 32 products and about
+// 150 other vector operations.  slice_kernel: the waves hold the same 32 rows and
+// each streams its own 32-key slices through LDS of its own, without a barrier:
+// few rows are bound by HBM (one token over 131072 keys, 537 MB: 86 us, 6.3
+// TB/s) or, over few keys, by latency (512 keys: 7.4 us).  Either may split the
+// keys over several workgroups; the unnormalised FP32 partial results then go to
+// the workspace and join_kernel adds them in a fixed order (3 to 4.5 us).
 #pragma once
 #include "attn.hpp"
 
