@@ -10,6 +10,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/DeviceGuard.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -173,6 +174,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n)
     TORCH_CHECK(n == 14 && g_norm, "qk_norm_rope: 14 arguments, after bind()");
     const at::Tensor& q = tensor_arg(a[0], "q");
     const int dtype = dtype_code(q);
+    const c10::DeviceGuard guard(q.device());   // the launch is on its current stream
     const at::Tensor* k = optional_arg(a[1], "k");
     const at::Tensor *qw = optional_arg(a[2], "q_weight"), *kw = optional_arg(a[3], "k_weight");
     const at::Tensor *qp = optional_arg(a[8], "q_pos"), *kp = optional_arg(a[9], "k_pos");
@@ -228,6 +230,7 @@ PyObject* cross_attn(PyObject*, PyObject* const* a, Py_ssize_t n)
     TORCH_CHECK(n == 8 && g_attn, "cross_attn: 8 arguments, after bind()");
     const at::Tensor& q = tensor_arg(a[0], "q");
     const int dtype = dtype_code(q);
+    const c10::DeviceGuard guard(q.device());   // the launch is on its current stream
     const at::Tensor &k = tensor_arg(a[1], "k"), &v = tensor_arg(a[2], "v");
     const at::Tensor *len = optional_arg(a[4], "kv_len"), *mask = optional_arg(a[5], "key_mask");
     const at::Tensor *out = optional_arg(a[6], "out"), *ws = optional_arg(a[7], "workspace");

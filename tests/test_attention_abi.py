@@ -65,6 +65,20 @@ def test_norm_checks(L):
         assert norm(L, side(), side(**{"batch": 1, **kw})) == want, kw
 
 
+def test_extension_loads_and_refuses_cpu_tensors():
+    import torch
+    q = torch.zeros(1, 2, 3, 64, dtype=torch.bfloat16)
+    for bad in (q, None, 3, [q]):
+        with pytest.raises(ValueError):
+            ck.ck_qk_norm_rope(bad)
+        with pytest.raises(ValueError):
+            ck.ck_cross_attn(bad, q, q)
+    with pytest.raises(ValueError):
+        ck.ck_qk_norm_rope(q, pairing="pairs")
+    with pytest.raises(ValueError):
+        ck.ck_qk_norm_rope(q, q_rope=q)
+
+
 def attn(L, q=None, k=None, v=None, o=None, batch=2, kv_batch=2, tq=0, tk=8, h=4, kh=2, d=64, dtype=0, scale=0.125,
          kv_len=None, mask=None, mask_st=0, ws=None, ws_n=0):
     r = [ctypes.byref(x or heads()) for x in (q, k, v, o)]

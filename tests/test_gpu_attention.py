@@ -248,6 +248,8 @@ SHAPES = [
     (2, 1, 1000, 512, 6, 6, 128),
     (1, 1, 2049, 191, 24, 24, 128),
     (1, 1, 4100, 1100, 8, 8, 64),
+    (600, 1, 1, 5, 4, 2, 64),
+    (90, 1, 130, 3, 4, 4, 128),
 ]
 
 
