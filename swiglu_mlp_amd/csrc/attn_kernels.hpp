@@ -34,12 +34,12 @@
 //
 // Two kernels.  tile_kernel: the waves of a workgroup hold different rows and
 // share each K / V tile.  Many rows are bound by the matrix cores, and those by
-// the chip's power: 24 heads of 128, 16384 rows over 4096 keys take 742 us (1110
-// TFLOP/s, a plain BF16 library product 1263) at 1.5 GHz with the matrix cores
+// the chip's power: 24 heads of 128, 16384 rows over 4096 keys take 742 to 776 us by
+// card (1110 TFLOP/s, a plain BF16 library product 1263) at 1.5 GHz with the matrix cores
 // busy 58% of the time; on zeros, 548.  A tile costs a wave 32 products and about
 // 150 other vector operations.  slice_kernel: the waves hold the same 32 rows and
 // each streams its own 32-key slices through LDS of its own, without a barrier:
-// few rows are bound by HBM (one token over 131072 keys, 537 MB: 86 us, 6.3
+// few rows are bound by HBM (one token over 131072 keys, 537 MB: 84 us, 6.4
 // TB/s) or, over few keys, by latency (512 keys: 7.4 us).  Either may split the
 // keys over several workgroups; the unnormalised FP32 partial results then go to
 // the workspace and join_kernel adds them in a fixed order (3 to 4.5 us).
@@ -772,7 +772,7 @@ __global__ __launch_bounds__(256, 1) void slice_kernel(Params p)
 
 // The splits of a row joined, in a fixed order, 4 channels a lane.  TEAMS teams
 // of 32 lanes share a row: one where there are many rows of few splits, eight
-// (each every eighth split, then added) where there are few rows of many.
+// (each every eighth split, then added) where there are few rows or many splits.
 template <typename T, int TEAMS>
 __global__ __launch_bounds__(256) void join_kernel(Params p, uint32_t all_rows)
 {
