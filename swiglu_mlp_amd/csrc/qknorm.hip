@@ -17,6 +17,7 @@
 // half pairing), and all U loads are in flight before the first is used.
 #include "ck_internal.hpp"
 #include "heads.hpp"
+#include "qk_lanes.hpp"
 
 namespace ck {
 namespace qkn {
@@ -77,13 +78,14 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(Side sq, Side sk, uin
     const uint32_t lane = threadIdx.x & (TEAM - 1);
     const uint32_t item = block * (256u / TEAM) + threadIdx.x / TEAM;
     // lanes with nothing to do stay for the exchanges between lanes below
-    const bool live = item < s.items && lane * 8 < d;
+    const Lane ln = lane_of(lane, d, rot, HALF);
+    const bool live = item < s.items && ln.live;
     const uint32_t it = item < s.items ? item : 0u;
     const uint32_t bt = s.by_hg.div(it);
     const uint32_t h0 = it - bt * s.hg;
     const uint32_t b = s.by_tokens.div(bt);
     const uint32_t t = bt - b * s.by_tokens.d;
-    const uint32_t c = lane * 8 < d ? lane * 8 : 0u;   // first channel of this lane
+    const uint32_t c = ln.c;   // first channel of this lane
 
     const uint16_t* x = s.x + (int64_t)b * s.x_sb + (int64_t)t * s.x_st + c;
     uint4 raw[U];
@@ -107,10 +109,8 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(Side sq, Side sk, uin
     // lane + or - rot / 16 of the team.  Channels past rot: cs = 1, sn = 0.
     const bool rope = s.cos != nullptr;   // workgroup-uniform
     float cs[HALF ? 8 : 4], sn[HALF ? 8 : 4], pw[8];
-    uint32_t other = lane;
     float bad = 0.0f;
     if (rope) {
-        const bool turns = c < rot;
         uint32_t p = t;
         if (s.pos) {   // a position outside the table writes NaN, and reads row 0
             p = (uint32_t)s.pos[(int64_t)b * s.pos_sb + t];
@@ -119,41 +119,39 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(Side sq, Side sk, uin
                 bad = __uint_as_float(0x7fc00000u);
             }
         }
-        const int64_t row = (int64_t)p * (rot / 2);
+        const int64_t at = (int64_t)p * (rot / 2) + ln.table;
 #pragma unroll
         for (int i = 0; i < (HALF ? 8 : 4); ++i) {
             cs[i] = 1.0f;
             sn[i] = 0.0f;
         }
         if constexpr (HALF) {
-            const bool upper = c >= rot / 2;
-            if (turns) {
-                const float* ct = s.cos + row + (upper ? c - rot / 2 : c);
-                const float* st = s.sin + row + (upper ? c - rot / 2 : c);
+            if (ln.turns) {
+                const float* ct = s.cos + at;
+                const float* st = s.sin + at;
 #pragma unroll
                 for (int i = 0; i < 8; i += 4) {
                     *reinterpret_cast<float4*>(cs + i) = *reinterpret_cast<const float4*>(ct + i);
                     *reinterpret_cast<float4*>(sn + i) = *reinterpret_cast<const float4*>(st + i);
                 }
-                other = upper ? lane - rot / 16 : lane + rot / 16;
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) pw[i] = upper ? 1.0f : -1.0f;
+            for (int i = 0; i < 8; ++i) pw[i] = ln.upper ? 1.0f : -1.0f;
             if (s.w) {
-                const float* ow = s.w + (turns ? other * 8 : c);
+                const float* ow = s.w + ln.other_c;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) pw[i] = pw[i] * ow[i];
             }
-        } else if (turns) {
-            *reinterpret_cast<float4*>(cs) = *reinterpret_cast<const float4*>(s.cos + row + c / 2);
-            *reinterpret_cast<float4*>(sn) = *reinterpret_cast<const float4*>(s.sin + row + c / 2);
+        } else if (ln.turns) {
+            *reinterpret_cast<float4*>(cs) = *reinterpret_cast<const float4*>(s.cos + at);
+            *reinterpret_cast<float4*>(sn) = *reinterpret_cast<const float4*>(s.sin + at);
         }
     }
 
     uint16_t* y = s.y + (int64_t)b * s.y_sb + (int64_t)t * s.y_st + c;
     const float inv_d = 1.0f / (float)d;
     // the partner lane's address for the exchange (a byte address in the wave)
-    const int from = (int)(((threadIdx.x & 63u) - lane + other) * 4u);
+    const int from = (int)(((threadIdx.x & 63u) - lane + ln.other) * 4u);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const uint32_t h = u * s.hg + h0;
