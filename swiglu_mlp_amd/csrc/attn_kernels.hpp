@@ -92,7 +92,7 @@ __device__ __forceinline__ void lds_dma_b128(v4i rsrc, uint32_t voff, uint32_t l
             "buffer_load_dwordx4 %0, %1, 0 offen nt lds"
             :
             : "v"(voff), "s"(rsrc), "s"(lds)
-            : "memory");
+            : "memory", "m0");
     else
         asm volatile(
             "s_mov_b32 m0, %2\n\t"
@@ -100,7 +100,7 @@ __device__ __forceinline__ void lds_dma_b128(v4i rsrc, uint32_t voff, uint32_t l
             "buffer_load_dwordx4 %0, %1, 0 offen lds"
             :
             : "v"(voff), "s"(rsrc), "s"(lds)
-            : "memory");
+            : "memory", "m0");
 }
 
 __device__ __forceinline__ v4i make_rsrc(const void* base)
