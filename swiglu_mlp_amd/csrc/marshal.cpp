@@ -18,6 +18,7 @@
 #include <optional>
 
 #include "ck.h"
+#include "views.hpp"
 
 namespace {
 
@@ -64,26 +65,13 @@ ck_heads heads_of(const at::Tensor& t, const char* what, const at::Tensor& q)
     return ck_heads{p, sb, st, sh};
 }
 
-// Whether two [batch, tokens, heads, d] views of one type share no element:
-// apart in memory, or different column ranges of rows with the same pitch.
-bool disjoint(const at::Tensor& a, const at::Tensor& b)
+ck::View view_of(const at::Tensor& t)
 {
-    const auto end = [](const at::Tensor& t) {
-        int64_t n = t.numel() ? 1 : 0;
-        for (int i = 0; n && i < 4; ++i) n += (t.size(i) - 1) * t.stride(i);
-        return (const char*)t.data_ptr() + n * t.element_size();
-    };
-    const char *a0 = (const char*)a.data_ptr(), *b0 = (const char*)b.data_ptr();
-    if (end(a) <= b0 || end(b) <= a0) return true;
-    const int64_t pitch = a.stride(1);
-    if (a.size(1) < 2 || b.size(1) < 2 || b.stride(1) != pitch || pitch <= 0) return false;
-    for (const at::Tensor* t : {&a, &b})   // one pitch over all (batch, token) rows
-        if (t->size(0) > 1 && t->stride(0) % pitch != 0) return false;
-    const auto width = [](const at::Tensor& t) { return (t.size(2) - 1) * t.stride(2) + t.size(3); };
-    int64_t gap = (b0 - a0) / a.element_size() % pitch;   // b's columns start `gap` after a's
-    if (gap < 0) gap += pitch;
-    return width(a) <= gap && gap + width(b) <= pitch;
+    TORCH_CHECK(t.dim() <= ck::View::kDims, "a view of ", t.dim(), " dimensions");
+    return ck::View::of(t.data_ptr(), (int64_t)t.element_size(), t.sizes().data(), t.strides().data(), (int)t.dim());
 }
+
+bool disjoint(const at::Tensor& a, const at::Tensor& b) { return ck::disjoint(view_of(a), view_of(b)); }
 
 // An output shaped like `like` (whose ck_heads are `in`): a new contiguous
 // tensor, or `out` checked.  `out` shares no element with `like` and `others`,
@@ -198,13 +186,16 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n)
     if (failed) return nullptr;
 
     ck_heads hy, hz;
+    ck_heads hk{};
+    if (k) {
+        hk = heads_of(*k, "k", q);
+        TORCH_CHECK_VALUE(k->size(3) == d, "q and k need one head size, got ", d, " and ", k->size(3));
+    }
     const at::Tensor y = output(qo, q, hq, "q_out", {k}, true, &hy);
     const ck_qk_side sq = side_of(q, hq, hy, qw, qr, qp, "q", q);
     at::Tensor z;
     ck_qk_side sk{};
     if (k) {
-        const ck_heads hk = heads_of(*k, "k", q);
-        TORCH_CHECK_VALUE(k->size(3) == d, "q and k need one head size, got ", d, " and ", k->size(3));
         z = output(ko, *k, hk, "k_out", {&q}, true, &hz);
         TORCH_CHECK_VALUE(!qo || !ko || disjoint(y, z), "q_out and k_out must not share memory");
         sk = side_of(*k, hk, hz, kw, kr, kp, "k", q);

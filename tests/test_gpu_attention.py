@@ -144,6 +144,52 @@ def test_norm_in_place_on_packed_rows_and_into_columns():
     assert torch.equal(z, qkv[:, :, hq:hq + hkv]) and torch.equal(y, qkv[:, :, :hq])
 
 
+def apart_views(layout, g):
+    """(buffer, q, k, v) in one buffer, sharing no element, in the layouts that projections and caches leave them in."""
+    hq, hkv, d = 6, 2, 128
+    if layout == "one token":              # decode: packed [q | k | v] rows of one token a sequence
+        x = torch.randn(16, 1, hq + 2 * hkv, d, generator=g, device=DEV).to(BF16)
+        return x, x[:, :, :hq], x[:, :, hq:hq + hkv], x[:, :, hq + hkv:]
+    if layout == "one sequence, one token":
+        x = torch.randn(1, 1, hq + 2 * hkv, d, generator=g, device=DEV).to(BF16)
+        return x, x[:, :, :hq], x[:, :, hq:hq + hkv], x[:, :, hq + hkv:]
+    if layout == "one token of many":      # the last token's queries over packed rows of all tokens
+        x = torch.randn(3, 9, hq + 2 * hkv, d, generator=g, device=DEV).to(BF16)
+        return x, x[:, 8:, :hq], x[:, :, hq:hq + hkv], x[:, :, hq + hkv:]
+    if layout == "heads first":            # [batch, q | k | v heads, tokens, d]
+        x = torch.randn(3, hq + 2 * hkv, 7, d, generator=g, device=DEV).to(BF16)
+        y = x.transpose(1, 2)
+        return x, y[:, :, :hq], y[:, :, hq:hq + hkv], y[:, :, hq + hkv:]
+    x = torch.randn(3, 5, hkv, 4 + 2, d, generator=g, device=DEV).to(BF16)   # grouped: a key head's q, k and v
+    return x, x[:, :, 0, :-2], x[:, :, :, -2], x[:, :, :, -1]
+
+
+@pytest.mark.parametrize("layout", ["one token", "one sequence, one token", "one token of many", "heads first",
+                                    "grouped"])
+def test_in_place_and_into_columns_of_one_buffer(layout):
+    x, q, k, v = apart_views(layout, gen(14))
+    was, was_q, was_k, was_v = apart_views(layout, gen(14))
+    rope = tables(9, 128, gen(15))
+    y, z = ck.ck_qk_norm_rope(q, k, q_rope=rope, k_rope=rope, q_out=q, k_out=k)
+    assert y is q and z is k
+    check_norm(y, was_q, None, rope, None, "half", 1e-6)
+    check_norm(z, was_k, None, rope, None, "half", 1e-6)
+    assert torch.equal(v, was_v)
+    # k into v's place, then attention into the queries' own place: the same buffer, nothing of it read and written
+    ck.ck_qk_norm_rope(was_q, was_k, q_rope=rope, k_rope=rope, k_out=was_v)
+    assert torch.equal(was_v, k)
+    queries = q.clone()
+    o = ck.ck_cross_attn(queries, k, v, out=q)
+    assert o is q
+    check_attn(o, queries, k, v)
+    # elements in common are refused as before
+    for f in (lambda: ck.ck_qk_norm_rope(q, k, k_out=q[:, :k.shape[1], :2]),
+              lambda: ck.ck_cross_attn(q, k, v, out=q),
+              lambda: ck.ck_cross_attn(v, k, v, out=v)):
+        with pytest.raises(ValueError):
+            f()
+
+
 def test_norm_strides_zeros_and_extremes():
     g = gen(4)
     # heads before tokens in memory, a batch-expanded tensor, a zero head and FP16 extremes

@@ -2,6 +2,7 @@
 checked over every size, also where a wrong index would not change a result."""
 import ctypes
 import os
+import random
 import shutil
 import subprocess
 
@@ -18,8 +19,9 @@ def compiled(tmp_path, header, code):
         pytest.skip("g++ not available")
     src, so = tmp_path / "host.cpp", tmp_path / "host.so"
     src.write_text(f'#include "{header}"\n{code}\n')
-    subprocess.run(["g++", "-O1", "-std=c++17", "-Wall", "-Wextra", "-Werror", "-fPIC", "-shared", f"-I{CSRC}",
-                    str(src), "-o", str(so)], check=True, capture_output=True, text=True, timeout=120)
+    r = subprocess.run(["g++", "-O1", "-std=c++17", "-Wall", "-Wextra", "-Werror", "-fPIC", "-shared", f"-I{CSRC}",
+                        str(src), "-o", str(so)], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stderr
     return ctypes.CDLL(str(so))
 
 
@@ -55,3 +57,72 @@ def test_norm_lanes_stay_inside_weights_and_tables(tmp_path):
                         assert x.other_c == 8 * x.other and lanes[x.other].other == i, case
                     else:
                         assert x.other == i and x.table == x.c // 2, case
+
+
+DISJOINT = """
+extern "C" bool apart(const int64_t *a, const int64_t *b, int64_t a0, int64_t b0, int64_t bytes_a, int64_t bytes_b)
+{
+    return ck::disjoint(ck::View::of((const void *)a0, bytes_a, a, a + 4, 4), ck::View::of((const void *)b0, bytes_b, b, b + 4, 4));
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def apart(tmp_path_factory):
+    """apart(a, b) of (first byte, element size, sizes, strides), up to four dimensions each."""
+    L = compiled(tmp_path_factory.mktemp("views"), "views.hpp", DISJOINT)
+    L.apart.restype = ctypes.c_bool
+    L.apart.argtypes = [ctypes.c_void_p, ctypes.c_void_p] + [ctypes.c_int64] * 4
+
+    def call(a, b):
+        def flat(v):
+            pad = 4 - len(v[2])
+            return (ctypes.c_int64 * 8)(*([1] * pad + list(v[2]) + [0] * pad + list(v[3])))
+        return L.apart(flat(a), flat(b), a[0], b[0], a[1], b[1])
+    return call
+
+
+def elements(v):
+    at = {v[0]}
+    for n, s in zip(v[2], v[3]):
+        at = {x + i * s * v[1] for x in at for i in range(n)}
+    return {x + i for x in at for i in range(v[1])}
+
+
+def test_views_apart(apart):
+    row = 48 * 128
+    q = (0, 2, (16, 1, 32, 128), (row, row, 128, 1))
+    k = (32 * 128 * 2, 2, (16, 1, 8, 128), (row, row, 128, 1))
+    assert apart(q, k) and apart(k, q) and not apart(q, q)
+    # the stride of a dimension of one element says nothing
+    assert apart((0, 2, (16, 1, 32, 128), (row, 7, 128, 1)), k)
+    # one token of each sequence beside packed rows of nine; heads before tokens; a key head's own group
+    assert apart((0, 2, (3, 1, 32, 128), (9 * row, row, 128, 1)), (8192, 2, (3, 9, 8, 128), (9 * row, row, 128, 1)))
+    assert apart((0, 2, (3, 7, 6, 64), (10 * 7 * 64, 64, 7 * 64, 1)), (6 * 7 * 128, 2, (3, 7, 2, 64), (10 * 7 * 64, 64, 7 * 64, 1)))
+    assert apart((0, 2, (2, 5, 3, 64), (50 * 64, 10 * 64, 64, 1)), (3 * 128, 2, (2, 5, 2, 64), (50 * 64, 10 * 64, 5 * 64, 1)))
+    # one more head of q would be k's first
+    assert not apart((0, 2, (16, 1, 33, 128), (row, row, 128, 1)), k)
+    assert not apart(k, (0, 2, (16, 1, 33, 128), (row, row, 128, 1)))
+    # an empty view; a line of bytes between two sequences, and one into the second
+    assert apart(q, (0, 1, (0,), (1,))) and apart((0, 2, (0, 4), (4, 1)), (0, 2, (9, 4), (4, 1)))
+    assert apart((0, 2, (2, 100), (1000, 1)), (200, 1, (1800,), (1,)))
+    assert not apart((0, 2, (2, 100), (1000, 1)), (200, 1, (1801,), (1,)))
+
+
+def test_views_called_apart_share_no_byte(apart):
+    rng = random.Random(1)
+
+    def view():
+        n = rng.randint(0, 4)
+        return (rng.randint(0, 60), rng.choice([1, 2]), tuple(rng.choice([0, 1, 1, 2, 2, 3]) for _ in range(n)),
+                tuple(rng.choice([0, 1, 1, 2, 3, 4, 6, 8, 12, 24, 36]) for _ in range(n)))
+
+    said = 0
+    for _ in range(30000):
+        a, b = view(), view()
+        if apart(a, b):
+            said += 1
+            assert not elements(a) & elements(b), (a, b)
+        else:
+            assert a != b or elements(a), (a, b)
+    assert said > 5000
