@@ -413,7 +413,7 @@ ck_status ck_qk_norm_rope(const ck_qk_side *q, const ck_qk_side *k, int64_t d, i
  * (the matrix cores' operand), and o once.  The result does not depend on
  * timing (fixed order of sums).
  *   workspace  ck_cross_attn_workspace_size(...) bytes (0: may be NULL),
- *              256-byte aligned, clobbered
+ *              256-byte aligned, clobbered, apart from all tensors of the call
  * Errors: CK_EINVAL on null or misaligned pointers, unknown type, scale;
  * CK_ESHAPE on sizes and strides; CK_EUNSUPPORTED on d > 128, on 2^30 or more
  * rows (batch * tq * heads) or 2^22 or more key heads (kv_batch * kv_heads);

@@ -717,7 +717,8 @@ def ck_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, q_rope=None, k_rope
     q_pos / k_pos (a position outside the table gives NaN in that token).
     pairing "half" turns channels (i, i + rot / 2), "interleaved" (2 i, 2 i + 1).
     Outputs are new contiguous tensors, or q_out / k_out, which may be q / k
-    themselves.  Returns q_out, or (q_out, k_out) when k is given."""
+    themselves and share no memory with anything else that the call reads.
+    Returns q_out, or (q_out, k_out) when k is given."""
     if pairing not in _PAIRING:
         raise ValueError(f"unknown pairing {pairing!r}")
     return _done("ck_qk_norm_rope", (_calls or _native()).qk_norm_rope(
@@ -734,7 +735,9 @@ def ck_cross_attn(q, k, v, scale=None, kv_len=None, key_mask=None, out=None, wor
     by default.  kv_len int32 [kv_batch]: the keys of each encoder sequence;
     key_mask bool or uint8 [kv_batch, tk]: False / 0 keys are left out.  What is
     left out is not read; a row with no key is zero.
-    Returns [batch, tq, heads, d], contiguous unless `out` is given."""
+    Returns [batch, tq, heads, d], contiguous unless `out` is given, which shares
+    no memory with the other tensors; nor does `workspace` (uint8, at least
+    ck_cross_attn_workspace_size(...) bytes)."""
     return _done("ck_cross_attn", (_calls or _native()).cross_attn(q, k, v, scale, kv_len, key_mask, out, workspace))
 
 

@@ -125,11 +125,12 @@ Rope rope_of(const at::Tensor* cos, const at::Tensor* sin, const char* what, con
     return Rope{(const float*)cos->data_ptr(), (const float*)sin->data_ptr(), cos->size(0), cos->size(1)};
 }
 
-ck_qk_side side_of(const at::Tensor& x, const ck_heads& in, const ck_heads& out, const at::Tensor* weight,
-                   const Rope& rope, const at::Tensor* pos, const char* what, const at::Tensor& q)
+// One side of a call, but for its output.
+ck_qk_side side_of(const at::Tensor& x, const ck_heads& in, const at::Tensor* weight, const Rope& rope,
+                   const at::Tensor* pos, const char* what, const at::Tensor& q)
 {
     ck_qk_side s{};
-    s.x = in, s.y = out;
+    s.x = in;
     s.batch = x.size(0), s.tokens = x.size(1), s.heads = x.size(2);
     if (weight) {
         TORCH_CHECK_VALUE(weight->scalar_type() == at::kFloat && weight->dim() == 1 && weight->size(0) == x.size(3) &&
@@ -167,8 +168,9 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n)
     const at::Tensor *qw = optional_arg(a[2], "q_weight"), *kw = optional_arg(a[3], "k_weight");
     const at::Tensor *qp = optional_arg(a[8], "q_pos"), *kp = optional_arg(a[9], "k_pos");
     const at::Tensor *qo = optional_arg(a[12], "q_out"), *ko = optional_arg(a[13], "k_out");
-    const Rope qr = rope_of(optional_arg(a[4], "q_rope"), optional_arg(a[5], "q_rope"), "q", q);
-    const Rope kr = rope_of(optional_arg(a[6], "k_rope"), optional_arg(a[7], "k_rope"), "k", q);
+    const at::Tensor *qc = optional_arg(a[4], "q_rope"), *qs = optional_arg(a[5], "q_rope");
+    const at::Tensor *kc = optional_arg(a[6], "k_rope"), *ks = optional_arg(a[7], "k_rope");
+    const Rope qr = rope_of(qc, qs, "q", q), kr = rope_of(kc, ks, "k", q);
     const int pairing = (int)PyLong_AsLong(a[10]);
     const float eps = (float)PyFloat_AsDouble(a[11]);
     if (PyErr_Occurred()) return nullptr;
@@ -185,20 +187,17 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n)
     void* stream = stream_of(q, &failed);
     if (failed) return nullptr;
 
-    ck_heads hy, hz;
-    ck_heads hk{};
+    ck_qk_side sq = side_of(q, hq, qw, qr, qp, "q", q), sk{};
     if (k) {
-        hk = heads_of(*k, "k", q);
+        const ck_heads hk = heads_of(*k, "k", q);
         TORCH_CHECK_VALUE(k->size(3) == d, "q and k need one head size, got ", d, " and ", k->size(3));
+        sk = side_of(*k, hk, kw, kr, kp, "k", q);
     }
-    const at::Tensor y = output(qo, q, hq, "q_out", {k}, true, &hy);
-    const ck_qk_side sq = side_of(q, hq, hy, qw, qr, qp, "q", q);
+    const at::Tensor y = output(qo, q, hq, "q_out", {k, qw, qc, qs, qp, kw, kc, ks, kp}, true, &sq.y);
     at::Tensor z;
-    ck_qk_side sk{};
     if (k) {
-        z = output(ko, *k, hk, "k_out", {&q}, true, &hz);
+        z = output(ko, *k, sk.x, "k_out", {&q, qw, qc, qs, qp, kw, kc, ks, kp}, true, &sk.y);
         TORCH_CHECK_VALUE(!qo || !ko || disjoint(y, z), "q_out and k_out must not share memory");
-        sk = side_of(*k, hk, hz, kw, kr, kp, "k", q);
     }
     ck_status st;
     Py_BEGIN_ALLOW_THREADS
@@ -246,20 +245,17 @@ PyObject* cross_attn(PyObject*, PyObject* const* a, Py_ssize_t n)
     void* stream = stream_of(q, &failed);
     if (failed) return nullptr;
 
-    ck_heads hy;
-    const at::Tensor y = output(out, q, hq, "out", {&k, &v}, false, &hy);
     const size_t need = g_attn_size(b, kb, tq, tk, h, kh, d);
+    if (!need) ws = nullptr;
+    TORCH_CHECK_VALUE(!ws || (ws->scalar_type() == at::kByte && ws->dim() == 1 && ws->is_contiguous() &&
+                              ws->device() == q.device() && (size_t)ws->numel() >= need),
+                      "workspace needs a contiguous uint8 tensor of ", need, " bytes on ", q.device());
+    ck_heads hy;
+    const at::Tensor y = output(out, q, hq, "out", {&k, &v, len, mask}, false, &hy);
+    for (const at::Tensor* t : {&q, &k, &v, &y, len, mask})
+        TORCH_CHECK_VALUE(!ws || !t || disjoint(*ws, *t), "workspace must not share memory with the call's tensors");
     at::Tensor room;
-    if (need) {
-        if (ws) {
-            TORCH_CHECK_VALUE(ws->scalar_type() == at::kByte && ws->dim() == 1 && ws->is_contiguous() &&
-                                  ws->device() == q.device() && (size_t)ws->numel() >= need,
-                              "workspace needs a contiguous uint8 tensor of ", need, " bytes on ", q.device());
-            room = *ws;
-        } else {
-            room = at::empty({(int64_t)need}, q.options().dtype(at::kByte));
-        }
-    }
+    if (need) room = ws ? *ws : at::empty({(int64_t)need}, q.options().dtype(at::kByte));
     ck_status st;
     Py_BEGIN_ALLOW_THREADS
     st = g_attn(&hq, &hk, &hv, &hy, b, kb, tq, tk, h, kh, d, dtype, (float)scale,

@@ -526,6 +526,59 @@ def test_refusals():
         no(c, z[:, :1], z, z, workspace=torch.empty(need - 1, dtype=torch.uint8, device=DEV))
 
 
+def test_refusals_of_shared_memory():
+    """Outputs and the workspace share no memory with anything the call reads, the small tensors included."""
+    def part(buf, at, dtype, *shape):
+        n = math.prod(shape) * torch.empty(0, dtype=dtype).element_size()
+        return buf[at:at + n].view(dtype).view(*shape)
+
+    buf = torch.zeros(1 << 20, dtype=torch.uint8, device=DEV)
+    q, out = (part(buf, i << 14, BF16, 2, 4, 4, 64) for i in range(2))
+    rope = tuple(part(buf, 1 << 18 | i << 12, torch.float32, 8, 32) for i in range(2))
+    w = part(buf, 3 << 18, torch.float32, 64)
+    pos = part(buf, 3 << 18 | 1024, torch.int32, 2, 4)
+    q.copy_(torch.randn(2, 4, 4, 64, generator=gen(16), device=DEV))
+    want = ck.ck_qk_norm_rope(q, q, w, w, q_rope=rope, k_rope=rope, q_pos=pos, k_pos=pos)[0]
+    kw = dict(q_weight=w, q_rope=rope, q_pos=pos)
+    assert torch.equal(ck.ck_qk_norm_rope(q, q_out=out, **kw), want)   # one buffer, nothing in common
+    at = out.data_ptr() - buf.data_ptr()
+    clash = [{"q_weight": part(buf, at, torch.float32, 64)}, {"q_weight": part(buf, at + 4096 - 256, torch.float32, 64)},
+             {"q_rope": (rope[0], part(buf, at + 16, torch.float32, 8, 32))},
+             {"q_rope": (part(buf, at - 16, torch.float32, 8, 32), rope[1])}, {"q_pos": part(buf, at, torch.int32, 2, 4)}]
+    for c in clash:
+        with pytest.raises(ValueError):
+            ck.ck_qk_norm_rope(q, q_out=out, **{**kw, **c})
+        for n, t in (("q", out), ("k", out)):   # of either side with either output
+            with pytest.raises(ValueError):
+                ck.ck_qk_norm_rope(q, q.clone(), **{n + "_out": t}, **{**kw, **{k.replace("q_", "k_"): v for k, v in kw.items()},
+                                                                      **{k.replace("q_", "k_"): v for k, v in c.items()}})
+
+    tk = 100_000
+    k = torch.randn(1, tk, 1, 64, generator=gen(17), device=DEV).to(BF16)
+    need = ck.lib().ck_cross_attn_workspace_size(1, 1, 1, tk, 1, 1, 64)
+    assert need > 0
+    q = torch.randn(1, 1, 1, 64, generator=gen(18), device=DEV).to(BF16)
+    mask = torch.ones(1, tk, dtype=torch.bool, device=DEV)
+    lens = torch.full((1,), tk, dtype=torch.int32, device=DEV)
+    room = torch.zeros(need + (1 << 18), dtype=torch.uint8, device=DEV)
+    ws, rest = room[:need], room[need:]
+    out = part(rest, 0, BF16, 1, 1, 1, 64)
+    want = ck.ck_cross_attn(q, k, k, kv_len=lens, key_mask=mask)
+    assert torch.equal(ck.ck_cross_attn(q, k, k, kv_len=lens, key_mask=mask, out=out, workspace=ws), want)
+    for kw in ({"out": part(room, need - 16, BF16, 1, 1, 1, 64), "workspace": ws},
+               {"kv_len": part(room, need - 4, torch.int32, 1), "workspace": ws},
+               {"key_mask": part(room, need - 1, torch.bool, 1, tk), "workspace": ws},
+               {"kv_len": part(rest, 64, torch.int32, 1), "out": out},
+               {"key_mask": part(rest, 127, torch.bool, 1, tk), "out": out},
+               {"workspace": k.view(torch.uint8).view(-1)[:need]}):
+        with pytest.raises(ValueError):
+            ck.ck_cross_attn(q, k, k, **kw)
+    with pytest.raises(ValueError):
+        ck.ck_cross_attn(part(room, 0, BF16, 1, 1, 1, 64), k, k, workspace=ws)
+    with pytest.raises(ValueError):      # a key that is no [batch, tokens, heads, d]
+        ck.ck_qk_norm_rope(q, k[None], q_out=torch.empty_like(q))
+
+
 # ---------------------------------------------------------------- the block of both
 def test_block_of_linears_norms_and_attention():
     """The example block against FP32 with unquantized weights.  Its INT8 linears are of the 1 to 2% class (relative
