@@ -90,6 +90,7 @@ at::Tensor output(const at::Tensor* out, const at::Tensor& like, const ck_heads&
     TORCH_CHECK_VALUE(out->sizes() == like.sizes(), what, " needs shape ", like.sizes(), ", got ", out->sizes());
     for (int i = 0; i < 4; ++i)
         TORCH_CHECK_VALUE(out->size(i) < 2 || out->stride(i) != 0, what, " must not be an expanded tensor");
+    TORCH_CHECK_VALUE(view_of(*out).distinct(), what, " must not hold an element twice, got strides ", out->strides());
     const bool same = h->data == in.data && h->batch_stride == in.batch_stride &&
                       h->token_stride == in.token_stride && h->head_stride == in.head_stride;
     bool ok = (in_place && same) || disjoint(*out, like);

@@ -14,7 +14,8 @@ struct View {
     int dims = 0;
     int64_t size[kDims] = {}, stride[kDims] = {};   // sizes over 1, strides in bytes, over 0
 
-    // A view of n <= 4 dimensions, strides in elements of `bytes` bytes.
+    // A view of n <= 4 dimensions, strides in elements of `bytes` bytes.  Where
+    // a stride is 0 the same bytes again are no others.
     static View of(const void* data, int64_t bytes, const int64_t* sizes, const int64_t* strides, int n)
     {
         View v;
@@ -40,6 +41,17 @@ struct View {
         for (int i = 0; i < dims; ++i)
             if (stride[i] < pitch) n += (size[i] - 1) * stride[i];
         return n;
+    }
+    // Whether no byte is part of two elements: each stride is at least the extent
+    // of all smaller ones.
+    bool distinct() const
+    {
+        for (int i = 0; i < dims; ++i)
+            if (stride[i] < extent(stride[i])) return false;
+        for (int i = 0; i < dims; ++i)
+            for (int j = 0; j < i; ++j)
+                if (stride[i] == stride[j]) return false;
+        return true;
     }
     bool rows_of(int64_t pitch) const   // whether all its larger strides are multiples of pitch
     {

@@ -579,6 +579,20 @@ def test_refusals_of_shared_memory():
         ck.ck_qk_norm_rope(q, k[None], q_out=torch.empty_like(q))
 
 
+def test_refusals_of_outputs_that_hold_an_element_twice():
+    q = torch.randn(2, 4, 4, 64, generator=gen(19), device=DEV).to(BF16)
+    buf = torch.empty(1 << 16, dtype=BF16, device=DEV)
+    for strides in ((1024, 128, 64, 1), (1024, 256, 32, 1), (64, 256, 64, 1), (256, 256, 64, 1), (0, 256, 64, 1)):
+        out = buf.as_strided(q.shape, strides)
+        for f in (lambda: ck.ck_qk_norm_rope(q, q_out=out), lambda: ck.ck_qk_norm_rope(q, q, k_out=out),
+                  lambda: ck.ck_cross_attn(q, q, q, out=out)):
+            with pytest.raises(ValueError):
+                f()
+    want = ck.ck_cross_attn(q, q, q)
+    for strides in ((1024, 256, 64, 1), (256, 512, 64, 1), (2048, 64, 256, 1)):
+        assert torch.equal(ck.ck_cross_attn(q, q, q, out=buf.as_strided(q.shape, strides)), want)
+
+
 # ---------------------------------------------------------------- the block of both
 def test_block_of_linears_norms_and_attention():
     """The example block against FP32 with unquantized weights.  Its INT8 linears are of the 1 to 2% class (relative
