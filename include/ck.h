@@ -340,7 +340,7 @@ size_t ck_swiglu_mlp_w8a16_workspace_size(int64_t m, int64_t h, int64_t i);
  * [batch, tokens, heads, d] with a stride for each of the first three
  * dimensions, so q, k and v may be column ranges of packed projection outputs.
  * d is a multiple of 8, strides are multiples of 8 elements in [0, 2^23)
- * (token and head) or [0, 2^40) (batch) and data is 16-byte aligned. */
+ * (token) or [0, 2^40) (head and batch) and data is 16-byte aligned. */
 typedef enum ck_dtype {
     CK_DTYPE_BF16 = 0,
     CK_DTYPE_FP16 = 1

@@ -22,7 +22,8 @@ Entry points keep the C names:
   ``ck_act_rotate_bf16``, ``ck_w8a16_gemm_bf16``, ``ck_int8_linear_w8a16``,
   ``ck_swiglu_mlp_w8a16``
 * attention side (BF16 or FP16 heads ``[batch, tokens, heads, d]``, strided
-  views such as column ranges of packed projections included):
+  views such as column ranges of packed projections included; tokens less than
+  2^23 elements apart):
   ``ck_qk_norm_rope(q, k=None, q_weight, k_weight, q_rope, k_rope, ...)``: per-head
   RMS norm and position rotation; ``ck_cross_attn(q, k, v, scale, kv_len,
   key_mask, ...)``: attention over encoder states of another length

@@ -573,9 +573,10 @@ ck_status ck_probe_stream_rows(const void* src, int64_t ld_bytes, int64_t m, int
 static ck_status check_heads(const ck_heads& h)
 {
     if (!h.data || !aligned16(h.data)) return CK_EINVAL;
-    for (const int64_t st : {h.token_stride, h.head_stride})
-        if (st < 0 || st >= (1 << 23) || st % 8 != 0) return CK_ESHAPE;
-    if (h.batch_stride < 0 || h.batch_stride >= (1LL << 40) || h.batch_stride % 8 != 0) return CK_ESHAPE;
+    // keys of a tile are at 32-bit byte offsets from its first; heads and sequences at 64-bit ones
+    if (h.token_stride < 0 || h.token_stride >= (1 << 23) || h.token_stride % 8 != 0) return CK_ESHAPE;
+    for (const int64_t st : {h.batch_stride, h.head_stride})
+        if (st < 0 || st >= (1LL << 40) || st % 8 != 0) return CK_ESHAPE;
     return CK_OK;
 }
 

@@ -108,3 +108,14 @@ def test_attention_workspace(L):
     assert size(2, 2, 4096, 512, 24, 24, 128) == 0          # enough row tiles: no split
     for ws, ws_n in ((None, n), (FAKE, n - 1), (FAKE + 16, n)):
         assert attn(L, batch=1, kv_batch=1, tq=1, tk=100_000, h=1, kh=1, ws=ws, ws_n=ws_n) == EWS
+
+
+def test_head_strides_of_long_caches(L):
+    # [batch, heads, tokens, d] from 65536 tokens of 128 channels on: a head stride past 2^23.  Accepted ones get as far
+    # as the next argument's refusal; nothing is launched
+    for sh, want in ((1 << 23, EINVAL), (1 << 30, EINVAL), ((1 << 40) - 8, EINVAL), (1 << 40, ESHAPE), ((1 << 23) + 4, ESHAPE)):
+        h = heads(sh=sh)
+        for bad in ({"x": h}, {"y": h}):
+            assert norm(L, side(), side(batch=1, weight=FAKE + 4, **bad)) == want, sh
+        for name in "qkvo":
+            assert attn(L, tq=1, kv_len=FAKE + 1, **{name: h}) == want, (name, sh)

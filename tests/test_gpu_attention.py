@@ -419,6 +419,20 @@ def test_attn_views_and_out(tq):
     assert torch.equal(ck.ck_cross_attn(q, k, v), y)
 
 
+@pytest.mark.parametrize("tq", [1, 40, 300])
+def test_heads_far_apart(tq):
+    # [batch, heads, tokens, 128] of 70000 tokens: heads 8.96 million elements apart; the norm in place, then attention
+    tk, g = 70_000, gen(20)
+    kv = torch.randn(1, 4, tk, 128, generator=g, device=DEV).to(BF16)
+    k, v = kv[:, :2].transpose(1, 2), kv[:, 2:].transpose(1, 2)
+    was = k.clone()
+    q = torch.randn(1, 4, tk, 128, generator=g, device=DEV).to(BF16).transpose(1, 2)[:, :tq]
+    _, k = ck.ck_qk_norm_rope(q, k, k_out=k)
+    check_norm(k, was, None, None, None, "half", 1e-6)
+    o = torch.empty(1, 4, tk, 128, dtype=BF16, device=DEV).transpose(1, 2)[:, :tq]
+    check_attn(ck.ck_cross_attn(q, k, v, out=o), q, k, v)
+
+
 def test_attn_no_keys_no_rows():
     q = torch.randn(2, 3, 4, 64, device=DEV).to(BF16)
     k = torch.empty(2, 0, 2, 64, dtype=BF16, device=DEV)
