@@ -336,6 +336,78 @@ def test_attn_lengths_and_masks(kb, share, tq, tk, h, kh, d, dtype):
     check_attn(ck.ck_cross_attn(q, k, v, key_mask=none), q, k, v, key_mask=none)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("kb,share,tq,tk,h,kh,d", [
+    (1, 1, 1000, 2048, 8, 8, 128),
+    (2, 1, 300, 1300, 4, 2, 72),
+    (1, 2, 300, 3000, 3, 3, 64),
+    (1, 1, 200, 5000, 16, 2, 128),
+    (1, 1, 515, 20000, 1, 1, 96),
+    (5, 1, 180, 1700, 8, 2, 80),
+])
+def test_attn_many_rows_with_split_keys(kb, share, tq, tk, h, kh, d, dtype):
+    # tiles of 128 rows whose keys go to several workgroups: whole, with lengths that end before, in and after a split,
+    # and with a mask that leaves the last sequence one key and the splits before it none
+    say(f"attn split tiles kb={kb} share={share} tq={tq} tk={tk} h={h} kh={kh} d={d} {dtype}")
+    assert share * tq * (h // kh) > 512 and ck.lib().ck_cross_attn_workspace_size(kb * share, kb, tq, tk, h, kh, d) > 0
+    q, k, v = make(kb, share, tq, tk, h, kh, d, dtype)
+    check_attn(ck.ck_cross_attn(q, k, v), q, k, v)
+    lens = torch.tensor([tk // 2 + 1, 0, tk + 3, 100, tk - 1][:kb], dtype=torch.int32, device=DEV)
+    mask = torch.rand(kb, tk, generator=gen(21), device=DEV) < 0.6
+    mask[-1] = False
+    mask[-1, tk - 1 if kb == 1 else 70] = True
+    check_attn(ck.ck_cross_attn(q, k, v, kv_len=lens), q, k, v, kv_len=lens)
+    check_attn(ck.ck_cross_attn(q, k, v, key_mask=mask), q, k, v, key_mask=mask)
+    check_attn(ck.ck_cross_attn(q, k, v, kv_len=lens, key_mask=mask), q, k, v, kv_len=lens, key_mask=mask)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("kb,tq,kh,d", [
+    (16, 1, 16, 64),      # slices, two splits of which the first has two lists
+    (16, 1, 16, 128),     # slices, one token
+    (2, 40, 80, 96),      # slices, two row tiles
+    (2, 2100, 8, 64),     # tiles, one key group
+    (2, 1600, 8, 128),    # tiles, two key groups
+])
+def test_attn_masks_over_several_lists(kb, tq, kh, d, dtype):
+    # 9001 keys are listed 4096 at a time: every list with keys (odd and even numbers of 32- and 64-key tiles, full
+    # and partly filled last ones), lists of few keys, of one, of none, and of all
+    tk, g = 9001, gen(22)
+    q, k, v = make(kb, 1, tq, tk, kh, kh, d, dtype)
+    kept = [(2458, 2459, 500), (64 * 39 - 5, 64 * 20, 3), (33, 4096, 809), (4096, 0, 32), (0, 65, 0), (1, 1, 1), (0, 0, 64)]
+    for first in range(0, len(kept), kb):
+        mask = torch.zeros(kb, tk, dtype=torch.bool, device=DEV)
+        for i in range(kb):
+            for j, n in enumerate(kept[(first + i) % len(kept)]):
+                size = min(4096, tk - 4096 * j)
+                mask[i, 4096 * j + torch.randperm(size, generator=g, device=DEV)[:n]] = True
+        check_attn(ck.ck_cross_attn(q, k, v, key_mask=mask), q, k, v, key_mask=mask)
+    lens = torch.randint(4000, tk + 1, (kb,), generator=g, device=DEV, dtype=torch.int32)
+    check_attn(ck.ck_cross_attn(q, k, v, kv_len=lens, key_mask=mask), q, k, v, kv_len=lens, key_mask=mask)
+
+
+@pytest.mark.parametrize("tq", [1, 40, 700, 1700])   # slices, tiles of two key groups and of one
+def test_keys_far_apart(tq):
+    # keys almost 2^23 elements apart: lists of 126 keys at a time, so that a listed key's offset stays in 32 bits
+    tk, kh, d, pitch = 600, 20, 64, (1 << 23) - 8
+    say(f"keys far apart tq={tq}")
+    g = gen(23)
+    room = torch.empty(tk * pitch, dtype=BF16, device=DEV)
+    k = room.as_strided((1, tk, kh, d), (tk * pitch, pitch, d, 1))
+    v = room.as_strided((1, tk, kh, d), (tk * pitch, pitch, d, 1), kh * d)
+    was = torch.randn(1, tk, kh, d, generator=g, device=DEV).to(BF16)
+    k.copy_(was)
+    v.copy_(torch.randn(1, tk, kh, d, generator=g, device=DEV) + 0.5)
+    q = torch.randn(1, tq, kh, d, generator=g, device=DEV).to(BF16)
+    _, k = ck.ck_qk_norm_rope(q, k, k_out=k)
+    check_norm(k, was, None, None, None, "half", 1e-6)
+    check_attn(ck.ck_cross_attn(q, k, v), q, k, v)
+    mask = torch.rand(1, tk, generator=g, device=DEV) < 0.6
+    check_attn(ck.ck_cross_attn(q, k, v, key_mask=mask), q, k, v, key_mask=mask)
+    mask[:, 126:300] = False
+    check_attn(ck.ck_cross_attn(q, k, v, key_mask=mask), q, k, v, key_mask=mask)
+
+
 @pytest.mark.parametrize("kb", [2, 15, 16, 17, 70])
 @pytest.mark.parametrize("tq", [1, 130])
 def test_attn_lengths_in_any_order(kb, tq):
