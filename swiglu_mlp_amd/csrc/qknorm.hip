@@ -106,8 +106,10 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(Side sq, Side sk, uin
 
     // The rotation as y = z * cs + partner * sn.  interleaved: 4 pairs in the
     // lane; half: the partner of channel c + i is rot / 2 channels away, in
-    // lane + or - rot / 16 of the team.  Channels past rot: cs = 1, sn = 0.
+    // lane + or - rot / 16 of the team.  Channels past rot skip it (times 1 plus
+    // their neighbour times 0 would spread an infinity).
     const bool rope = s.cos != nullptr;   // workgroup-uniform
+    const bool turns = rope && ln.turns;
     float cs[HALF ? 8 : 4], sn[HALF ? 8 : 4], pw[8];
     float bad = 0.0f;
     if (rope) {
@@ -120,13 +122,8 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(Side sq, Side sk, uin
             }
         }
         const int64_t at = (int64_t)p * (rot / 2) + ln.table;
-#pragma unroll
-        for (int i = 0; i < (HALF ? 8 : 4); ++i) {
-            cs[i] = 1.0f;
-            sn[i] = 0.0f;
-        }
         if constexpr (HALF) {
-            if (ln.turns) {
+            if (turns) {
                 const float* ct = s.cos + at;
                 const float* st = s.sin + at;
 #pragma unroll
@@ -142,7 +139,7 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(Side sq, Side sk, uin
 #pragma unroll
                 for (int i = 0; i < 8; ++i) pw[i] = pw[i] * ow[i];
             }
-        } else if (ln.turns) {
+        } else if (turns) {
             *reinterpret_cast<float4*>(cs) = *reinterpret_cast<const float4*>(s.cos + at);
             *reinterpret_cast<float4*>(sn) = *reinterpret_cast<const float4*>(s.sin + at);
         }
@@ -175,12 +172,12 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(Side sq, Side sk, uin
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 o[i] = v[i] * r * w[i];
-                if (rope) o[i] = __builtin_fmaf(pv[i] * r * pw[i], sn[i], o[i] * cs[i]);
+                if (turns) o[i] = __builtin_fmaf(pv[i] * r * pw[i], sn[i], o[i] * cs[i]);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] = v[i] * r * w[i];
-            if (rope) {
+            if (turns) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float a = o[2 * i], z = o[2 * i + 1];

@@ -205,6 +205,28 @@ def test_norm_strides_zeros_and_extremes():
     check_norm(ck.ck_qk_norm_rope(b), b, None, None, None, "half", 1e-6)
 
 
+@pytest.mark.parametrize("pairing", ["half", "interleaved"])
+@pytest.mark.parametrize("rot", [32, 64])
+def test_norm_infinities_stay_in_their_pairs(pairing, rot):
+    # a head with an infinity has an infinite mean square: its finite channels are 0, the infinite one is NaN, and so is
+    # the other channel of its pair if it is turned
+    g = gen(24)
+    q = torch.randn(1, 70, 3, 64, generator=g, device=DEV).to(BF16)
+    for c in range(64):
+        q[0, c, 1, c] = math.inf if c % 2 else -math.inf
+    q[0, 65, 2, 40] = math.nan
+    rope = tables(70, rot, g)
+    w = 1 + 0.3 * torch.randn(64, generator=g, device=DEV)
+    w[50] = math.inf                               # a weight's infinity stays in its channel
+    for weight in (None, w):
+        y = ck.ck_qk_norm_rope(q, q_weight=weight, q_rope=rope, pairing=pairing)
+        ref, _ = norm_ref(q, weight, rope, None, pairing, 1e-6)
+        assert torch.equal(y.isnan(), ref.isnan())
+        assert torch.equal(y.isinf(), ref.isinf())
+        rest = ref.isfinite()
+        assert torch.equal(y[rest] == 0, ref[rest] == 0)
+
+
 @pytest.mark.parametrize("pairing,dtype", [("half", BF16), ("interleaved", FP16)])
 def test_norm_past_the_caches(pairing, dtype):
     # over 256 MiB read and written: the nontemporal form
