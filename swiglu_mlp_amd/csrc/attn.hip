@@ -38,9 +38,7 @@ attn::Plan plan_of(int64_t bh, int64_t rows, int64_t tk, int64_t d)
     p.splits = (uint32_t)std::max<int64_t>(1, (tk + p.split_keys - 1) / p.split_keys);
     // two groups of waves halve a workgroup's way through its keys, for about a
     // microsecond to join them (1000 rows, 8 heads of 128, 8192 keys: 46.0 us, one
-    // group 49.4; 1024 rows, 32 heads of 96, 128 keys: 8.4 and 7.1).  Tiles whose
-    // keys are split always have two: at least 512 keys a split, at most one
-    // workgroup a CU.
+    // group 49.4; 1024 rows, 32 heads of 96, 128 keys: 8.4 and 7.1)
     p.two_groups = !p.slices && groups * p.splits <= cus && p.split_keys >= 512;
     return p;
 }

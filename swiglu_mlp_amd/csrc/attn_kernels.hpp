@@ -613,7 +613,7 @@ __global__ __launch_bounds__(NW * KG * 64, DP <= 64 && KG == 1 && !MASK ? 4 : 2)
         r.m = m;
     }
     if (w.row >= p.rows) return;
-    if (KG > 1 && p.splits > 1) {   // (attn.hip: split keys have two groups)
+    if (p.splits > 1) {
         const uint64_t at = ((uint64_t)w.bh * p.rows + w.row) * p.splits + w.split;
         if (w.half == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(r.m, r.l);
         float* po = p.part_o + at * p.d + 4 * w.half;
