@@ -737,8 +737,8 @@ def ck_cross_attn(q, k, v, scale=None, kv_len=None, key_mask=None, out=None, wor
     key_mask bool or uint8 [kv_batch, tk]: False / 0 keys are left out.  What is
     left out is not read; a row with no key is zero.
     Returns [batch, tq, heads, d], contiguous unless `out` is given, which shares
-    no memory with the other tensors; nor does `workspace` (uint8, at least
-    ck_cross_attn_workspace_size(...) bytes)."""
+    no memory with the other tensors; nor does `workspace` (uint8, 256-byte
+    aligned, at least ck_cross_attn_workspace_size(...) bytes)."""
     return _done("ck_cross_attn", (_calls or _native()).cross_attn(q, k, v, scale, kv_len, key_mask, out, workspace))
 
 

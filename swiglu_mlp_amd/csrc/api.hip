@@ -641,7 +641,7 @@ ck_status ck_qk_norm_rope(const ck_qk_side* q, const ck_qk_side* k, int64_t d, i
                                             (hipStream_t)stream));
 }
 
-// Sizes of ck_cross_attn; *rows: query rows that share one key head's keys.
+// Sizes of ck_cross_attn.
 static ck_status check_attn_sizes(int64_t batch, int64_t kv_batch, int64_t tq, int64_t tk, int64_t heads,
                                   int64_t kv_heads, int64_t d)
 {

@@ -35,12 +35,12 @@
 // Two kernels.  tile_kernel: the waves of a workgroup hold different rows and
 // share each K / V tile.  Many rows are bound by the matrix cores, and those by
 // the chip's power: 24 heads of 128, 16384 rows over 4096 keys take 742 to 776 us by
-// card (1110 TFLOP/s, a plain BF16 library product 1263) at 1.5 GHz with the matrix cores
-// busy 58% of the time; on zeros, 548.  A tile costs a wave 32 products and about
+// card (1060 to 1110 TFLOP/s, a plain BF16 library product 1263) at 1.5 to 1.7 GHz with the
+// matrix cores busy 57% of the time; on zeros, 548.  A tile costs a wave 32 products and about
 // 150 other vector operations.  slice_kernel: the waves hold the same 32 rows and
 // each streams its own 32-key slices through LDS of its own, without a barrier:
-// few rows are bound by HBM (one token over 131072 keys, 537 MB: 84 us, 6.4
-// TB/s) or, over few keys, by latency (512 keys: 7.4 us).  Either may split the
+// few rows are bound by HBM (one token over 131072 keys, 537 MB: 84 to 86 us, 6.2
+// to 6.4 TB/s) or, over few keys, by latency (512 keys: 7.4 us).  Either may split the
 // keys over several workgroups; the unnormalised FP32 partial results then go to
 // the workspace and join_kernel adds them in a fixed order (3 to 4.5 us).
 #pragma once
@@ -167,6 +167,11 @@ struct Place {
 // order stays, which spreads a long sequence over the XCDs, and with LONGEST
 // the longest of up to 16 sequences come first (333 rows of 7 sequences of up to
 // 1023 keys: 22.3 us, 23.9 shortest first; ranking 64 sequences takes 3 us).
+// Plain order against contiguous eighths, both with lengths: those 333 rows 22.3
+// and 27.9 us, 1024 rows of 16 sequences of 128 to 2048 keys, 16 heads of 64: 95
+// and 129, 2 x 4096 rows of 512 and 300 keys, 24 heads of 128: 56.6 and 61.6; but
+// both of 512 keys: 66.8 and 64.9, and one sequence of 16384 rows and 4096 keys:
+// 768 and 766.
 template <bool LONGEST>
 __device__ __forceinline__ Place place_of(const Params& p, uint32_t row_in_tile, uint32_t tile_rows)
 {
@@ -844,7 +849,7 @@ hipError_t launch_padded(Params& p, const Plan& plan, uint32_t bh, hipStream_t s
     if (e != hipSuccess || plan.splits == 1) return e;
     p.by_tiles = FastDiv(p.rows);
     const uint32_t rows = bh * p.rows;
-    // 160 rows of 12 splits: 8.4 us a call with eight teams a row, 9.3 with one;
+    // 160 rows of 6 splits: 7.9 us a call with eight teams a row, 8.6 with one;
     // 4096 rows of 4: 21.3 and 19.4
     if (plan.splits >= 16 || rows <= 512)
         join_kernel<T, 8><<<dim3(rows), dim3(256), 0, st>>>(p, rows);

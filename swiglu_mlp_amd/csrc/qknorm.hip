@@ -9,7 +9,7 @@
 //
 // The kernel is bound by HBM: 2 bytes read and 2 written per element, about 10
 // VALU operations (4 x 16384 tokens of 32 + 8 heads of 128, 1.34 GB: 226 us, 5.9
-// TB/s; 16 tokens of those: 3.0 us).  Layout: a team of 8, 16 or 32 lanes holds one head (8
+// TB/s; 16 tokens of those: 3.0 to 3.4 us).  Layout: a team of 8, 16 or 32 lanes holds one head (8
 // channels, one 16-byte load, per lane), so a wave's load covers consecutive
 // heads of a token, whole cache lines.  A team takes up to U heads of one
 // token: the norm weights and the token's cos / sin values are read once for
