@@ -71,14 +71,29 @@ ck::View view_of(const at::Tensor& t)
     return ck::View::of(t.data_ptr(), (int64_t)t.element_size(), t.sizes().data(), t.strides().data(), (int)t.dim());
 }
 
-bool disjoint(const at::Tensor& a, const at::Tensor& b) { return ck::disjoint(view_of(a), view_of(b)); }
+// What a call reads, once for all the comparisons with its outputs.
+struct Reads {
+    ck::View views[10];
+    int n = 0;
+    void add(std::initializer_list<const at::Tensor*> tensors)   // null: not given
+    {
+        for (const at::Tensor* t : tensors)
+            if (t) views[n++] = view_of(*t);
+    }
+    bool apart_from(const ck::View& v) const
+    {
+        for (int i = 0; i < n; ++i)
+            if (!ck::disjoint(v, views[i])) return false;
+        return true;
+    }
+};
 
 // An output shaped like `like` (whose ck_heads are `in`): a new contiguous
-// tensor, or `out` checked.  `out` shares no element with `like` and `others`,
-// or it is `like` itself where `in_place` allows that (each head is read before
-// it is written).
+// tensor, or `out` checked.  `out` shares no element with `like` and `reads`, or
+// it is `like` itself where `in_place` allows that (each head is read before it
+// is written).
 at::Tensor output(const at::Tensor* out, const at::Tensor& like, const ck_heads& in, const char* what,
-                  std::initializer_list<const at::Tensor*> others, bool in_place, ck_heads* h)
+                  std::initializer_list<const Reads*> reads, bool in_place, ck_heads* h)
 {
     if (!out) {
         at::Tensor t = at::empty(like.sizes(), like.options());
@@ -90,11 +105,12 @@ at::Tensor output(const at::Tensor* out, const at::Tensor& like, const ck_heads&
     TORCH_CHECK_VALUE(out->sizes() == like.sizes(), what, " needs shape ", like.sizes(), ", got ", out->sizes());
     for (int i = 0; i < 4; ++i)
         TORCH_CHECK_VALUE(out->size(i) < 2 || out->stride(i) != 0, what, " must not be an expanded tensor");
-    TORCH_CHECK_VALUE(view_of(*out).distinct(), what, " must not hold an element twice, got strides ", out->strides());
+    const ck::View v = view_of(*out);
+    TORCH_CHECK_VALUE(v.distinct(), what, " must not hold an element twice, got strides ", out->strides());
     const bool same = h->data == in.data && h->batch_stride == in.batch_stride &&
                       h->token_stride == in.token_stride && h->head_stride == in.head_stride;
-    bool ok = (in_place && same) || disjoint(*out, like);
-    for (const at::Tensor* t : others) ok = ok && (!t || disjoint(*out, *t));
+    bool ok = (in_place && same) || ck::disjoint(v, view_of(like));
+    for (const Reads* r : reads) ok = ok && r->apart_from(v);
     TORCH_CHECK_VALUE(ok, what, " must not share memory with what the call reads");
     return *out;
 }
@@ -194,11 +210,20 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n)
         TORCH_CHECK_VALUE(k->size(3) == d, "q and k need one head size, got ", d, " and ", k->size(3));
         sk = side_of(*k, hk, kw, kr, kp, "k", q);
     }
-    const at::Tensor y = output(qo, q, hq, "q_out", {k, qw, qc, qs, qp, kw, kc, ks, kp}, true, &sq.y);
+    Reads small, own_q, own_k;
+    if (qo || ko) {
+        small.add({qw, qc, qs, qp, kw});
+        if (kc != qc) small.add({kc});
+        if (ks != qs) small.add({ks});
+        if (kp != qp) small.add({kp});
+        own_q.add({&q});
+        own_k.add({k});
+    }
+    const at::Tensor y = output(qo, q, hq, "q_out", {&small, &own_k}, true, &sq.y);
     at::Tensor z;
     if (k) {
-        z = output(ko, *k, sk.x, "k_out", {&q, qw, qc, qs, qp, kw, kc, ks, kp}, true, &sk.y);
-        TORCH_CHECK_VALUE(!qo || !ko || disjoint(y, z), "q_out and k_out must not share memory");
+        z = output(ko, *k, sk.x, "k_out", {&small, &own_q}, true, &sk.y);
+        TORCH_CHECK_VALUE(!qo || !ko || ck::disjoint(view_of(y), view_of(z)), "q_out and k_out must not share memory");
     }
     ck_status st;
     Py_BEGIN_ALLOW_THREADS
@@ -252,9 +277,13 @@ PyObject* cross_attn(PyObject*, PyObject* const* a, Py_ssize_t n)
                               ws->device() == q.device() && (size_t)ws->numel() >= need),
                       "workspace needs a contiguous uint8 tensor of ", need, " bytes on ", q.device());
     ck_heads hy;
-    const at::Tensor y = output(out, q, hq, "out", {&k, &v, len, mask}, false, &hy);
-    for (const at::Tensor* t : {&q, &k, &v, &y, len, mask})
-        TORCH_CHECK_VALUE(!ws || !t || disjoint(*ws, *t), "workspace must not share memory with the call's tensors");
+    Reads reads;
+    if (out || ws) reads.add({&k, &v, len, mask});
+    const at::Tensor y = output(out, q, hq, "out", {&reads}, false, &hy);
+    if (ws) {
+        reads.add({&q, &y});
+        TORCH_CHECK_VALUE(reads.apart_from(view_of(*ws)), "workspace must not share memory with the call's tensors");
+    }
     at::Tensor room;
     if (need) room = ws ? *ws : at::empty({(int64_t)need}, q.options().dtype(at::kByte));
     ck_status st;
