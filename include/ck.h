@@ -1,6 +1,7 @@
 /*
- * ck.h -- C ABI of the MI355X (gfx950) ConvRot INT8 linear and SwiGLU MLP, and
- * of the attention-side operators between such linears.
+ * ck.h -- C ABI of the MI355X (gfx950) ConvRot INT8 linear and SwiGLU MLP, of
+ * the linear on microscaled 4-bit weights, and of the operators between such
+ * linears (attention side, residual sums with their norms).
  *
  * What the library computes (sources cited by page title and section):
  *
@@ -343,7 +344,8 @@ size_t ck_swiglu_mlp_w8a16_workspace_size(int64_t m, int64_t h, int64_t i);
  * (token) or [0, 2^40) (head and batch) and data is 16-byte aligned. */
 typedef enum ck_dtype {
     CK_DTYPE_BF16 = 0,
-    CK_DTYPE_FP16 = 1
+    CK_DTYPE_FP16 = 1,
+    CK_DTYPE_FP32 = 2          /* modulations of ck_block_norm only             */
 } ck_dtype;
 
 typedef struct ck_heads {
@@ -425,6 +427,125 @@ ck_status ck_cross_attn(const ck_heads *q, const ck_heads *k, const ck_heads *v,
                         void *workspace, size_t workspace_bytes, void *stream);
 size_t ck_cross_attn_workspace_size(int64_t batch, int64_t kv_batch, int64_t tq, int64_t tk,
                                     int64_t heads, int64_t kv_heads, int64_t d);
+
+/* ---- MX FP4 linears: microscaled 4-bit weights and activations ----
+ * Operands in the OCP microscaling format MXFP4: E2M1 values (0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6 and their negatives) with one E8M0 scale 2^(s - 127) for each 32
+ * consecutive k of a row, s = 255 standing for NaN.  The matrix cores multiply
+ * them at twice the INT8 rate, and a weight is half the INT8 one's bytes.
+ *
+ * Quantization of a row (a = x, silu(gate) * up, or a weight), in FP32:
+ *   v = a H, H the normalised block-diagonal Hadamard matrix of `group` channels
+ *       as above (group 1: v = a)
+ *   A = max |v| of the 32;  e = max(floor(log2 A) - 2, -127);  s = e + 127
+ *   code = v 2^-e to the nearest E2M1 value, ties to the even code, at most 6
+ * A block with a NaN or an infinity (of a, or of a rotated sum past FP32) gets
+ * s = 255, and so NaN in every product with it.  A zero's code may have either
+ * sign.
+ *
+ * CK_LAYOUT_ROWS (serialized checkpoints): codes [rows, k / 2] bytes, the even k
+ * in the low nibble; scales [rows, k / 32] bytes.
+ * CK_LAYOUT_BLOCKED (what the product reads): rows padded to rp, a multiple of
+ * 32, and k to kp, a multiple of 256.  Codes, rp * kp / 2 bytes: 1 KB blocks
+ * (r / 32, k / 64) at ((r / 32) * (kp / 64) + k / 64) * 1024, inside a block the
+ * byte ((k % 64) / 32) * 512 + (r % 32) * 16 + (k % 32) / 2.  Scales, rp * kp / 32
+ * bytes: 256 bytes (r / 32, k / 256) at ((r / 32) * (kp / 256) + k / 256) * 256,
+ * inside them the byte (32 ((k % 64) / 32) + r % 32) * 4 + (k % 256) / 64.
+ * Padding columns hold zero products; padding rows are never read into valid
+ * outputs (an activation's are not written).
+ * Shapes as in the INT8 calls (k % 64 == 0, k % group == 0, n % 16 == 0,
+ * k <= CK_MAX_K), with rp * kp < 2^34 for either operand and m n < 2^35. */
+int64_t ck_mx4_rows(int64_t rows);   /* rp (0 for rows <= 0) */
+int64_t ck_mx4_cols(int64_t k);      /* kp (0 for k <= 0) */
+
+/* Rotate and quantize an FP32 weight [n, k] (done once, at load). */
+ck_status ck_mx4_weight_prep(const float *w, int64_t n, int64_t k, int32_t group, int32_t layout,
+                             uint8_t *codes, uint8_t *scales, void *stream);
+
+/* Serialized codes and scales (CK_LAYOUT_ROWS) -> CK_LAYOUT_BLOCKED, padding
+ * zeroed (done once, at load).  Reads codes [n, k / 2] and scales [n, k / 32]. */
+ck_status ck_mx4_weight_pack(const uint8_t *codes, const uint8_t *scales, int64_t n, int64_t k,
+                             uint8_t *codes_blk, uint8_t *scales_blk, void *stream);
+
+/* Activation quantizer: x, ldx and act as ck_act_quant. */
+ck_status ck_mx4_act_quant(const uint16_t *x, int64_t ldx, int64_t m, int64_t k, int32_t act,
+                           int32_t group, int32_t layout, uint8_t *codes, uint8_t *scales, void *stream);
+
+/* The values that codes and scales of `rows` rows stand for, BF16 [rows, k]
+ * (exact; a value past BF16's range is infinite). */
+ck_status ck_mx4_dequant(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t k,
+                         int32_t layout, uint16_t *y, void *stream);
+
+/* y[m, n] = bf16(sum_k x[m, k] w[n, k] (+ bias[n]) (+ residual[m, n])), operands
+ * in CK_LAYOUT_BLOCKED, sums in FP32 in a fixed order (the same call gives the
+ * same bits), one rounding at the end.  bias, residual and y as ck_int8_linear.
+ *   workspace  ck_mx4_gemm_workspace_size(m, k, n) bytes (0: may be NULL),
+ *              256-byte aligned, clobbered */
+ck_status ck_mx4_gemm_bf16(const uint8_t *x_codes, const uint8_t *x_scales, const uint8_t *w_codes,
+                           const uint8_t *w_scales, const float *bias, const uint16_t *residual,
+                           int64_t m, int64_t n, int64_t k, uint16_t *y, void *workspace,
+                           size_t workspace_bytes, void *stream);
+size_t ck_mx4_gemm_workspace_size(int64_t m, int64_t k, int64_t n);
+
+/* The MX FP4 linear: ck_mx4_act_quant of x into the workspace, then
+ * ck_mx4_gemm_bf16.  Arguments as there, the weight in CK_LAYOUT_BLOCKED.
+ *   workspace  ck_mx4_linear_workspace_size(m, k, n) bytes, 256-byte aligned,
+ *              clobbered; apart from every other buffer of the call
+ * Errors as ck_int8_linear. */
+ck_status ck_mx4_linear(const uint16_t *x, int64_t ldx, int32_t act, const uint8_t *w_codes,
+                        const uint8_t *w_scales, const float *bias, const uint16_t *residual,
+                        int64_t m, int64_t n, int64_t k, int32_t group, uint16_t *y, void *workspace,
+                        size_t workspace_bytes, void *stream);
+size_t ck_mx4_linear_workspace_size(int64_t m, int64_t k, int64_t n);
+
+/* ---- Between two sub-blocks: residual sum, gate and norms ---- */
+typedef enum ck_norm_kind {
+    CK_NORM_NONE = 0,
+    CK_NORM_RMS = 1,           /* v rsqrt(mean(v^2) + eps) weight (+ bias)      */
+    CK_NORM_LAYER = 2          /* the same of v - mean(v)                       */
+} ck_norm_kind;
+
+typedef struct ck_norm {
+    int32_t kind;              /* ck_norm_kind                                  */
+    const float *weight;       /* [width] FP32, 16-byte aligned, or NULL (ones) */
+    const float *bias;         /* [width] FP32, 16-byte aligned, or NULL        */
+} ck_norm;
+
+/* Rows [batch, tokens, width] with contiguous channels; strides in elements,
+ * multiples of 8 in [0, 2^40); 16-byte aligned. */
+typedef struct ck_rows {
+    void *data;
+    int64_t batch_stride, token_stride;
+} ck_rows;
+
+/* r = residual_scale x + branch_scale gate N_b(branch)    -> x_out
+ * h = N(r) (1 + scale) + shift                            -> out
+ * with N_b = branch_norm and N = norm, every step in FP32 and each output rounded
+ * once (h is of the unrounded r).
+ *   x, branch     read; branch.data may be NULL: r = residual_scale x, and
+ *                 branch_norm, gate and x_out must be absent
+ *   x_out, out    written; data may be NULL (not wanted), not for both.  Either
+ *                 may be x or branch itself (the same data and strides); otherwise
+ *                 they overlap nothing that is read, nor each other
+ *   gate, scale, shift  data may be NULL; strides of 0 share a modulation over
+ *                 the tokens or the batch.  Of type mod_dtype: dtype, or
+ *                 CK_DTYPE_FP32 (strides then multiples of 4)
+ *   norm          CK_NORM_NONE only without scale, shift and out
+ *   width         multiple of 8, at most CK_MAX_NORM_WIDTH
+ *   eps           finite, at least 2^-126; the scales finite
+ * Errors: CK_EINVAL on null or misaligned pointers, unknown kinds and types, the
+ * scalars; CK_ESHAPE on sizes and strides; CK_EUNSUPPORTED on a larger width or
+ * 2^24 or more rows (batch * tokens). */
+#define CK_MAX_NORM_WIDTH 16384
+typedef struct ck_block_norm_args {
+    ck_rows x, branch, x_out, out;
+    int64_t batch, tokens, width;
+    ck_norm branch_norm, norm;
+    ck_rows gate, scale, shift;
+    int32_t dtype, mod_dtype;
+    float residual_scale, branch_scale, eps;
+} ck_block_norm_args;
+ck_status ck_block_norm(const ck_block_norm_args *args, void *stream);
 
 /* ---- test hooks: the same device code with its intermediate exposed ---- */
 

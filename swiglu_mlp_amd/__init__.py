@@ -27,6 +27,11 @@ Entry points keep the C names:
   ``ck_qk_norm_rope(q, k=None, q_weight, k_weight, q_rope, k_rope, ...)``: per-head
   RMS norm and position rotation; ``ck_cross_attn(q, k, v, scale, kv_len,
   key_mask, ...)``: attention over encoder states of another length
+* MX FP4 (4-bit weights and activations with a scale for each 32 values of k):
+  ``ck_mx4_weight_prep``, ``ck_mx4_weight_pack``, ``ck_mx4_act_quant``,
+  ``ck_mx4_dequant``, ``ck_mx4_gemm_bf16``, ``ck_mx4_linear``
+* between two sub-blocks: ``ck_block_norm(x, branch, gate, ...)``: the residual
+  sum with the branch's norm and gate, and the next norm with its modulation
 * test hooks ``ck_int8_gemm_i32``, ``ck_w8a16_gemm_f32``, ``ck_silu_f32``, ``ck_act_rotate_f32``
 
 INT8 operand layouts, each with its own tensor form so that a call can tell
@@ -114,6 +119,13 @@ def bind(path: str) -> ctypes.CDLL:
         "ck_qk_norm_rope": [p, p, i64, i64, i32, i32, ctypes.c_float, p],
         "ck_cross_attn": [p, p, p, p, i64, i64, i64, i64, i64, i64, i64, i32, ctypes.c_float,
                           p, p, i64, p, sz, p],
+        "ck_mx4_weight_prep": [p, i64, i64, i32, i32, p, p, p],
+        "ck_mx4_weight_pack": [p, p, i64, i64, p, p, p],
+        "ck_mx4_act_quant": [p, i64, i64, i64, i32, i32, i32, p, p, p],
+        "ck_mx4_dequant": [p, p, i64, i64, i32, p, p],
+        "ck_mx4_gemm_bf16": [p, p, p, p, p, p, i64, i64, i64, p, p, sz, p],
+        "ck_mx4_linear": [p, i64, i32, p, p, p, p, i64, i64, i64, i32, p, p, sz, p],
+        "ck_block_norm": [p, p],
         "ck_silu_f32": [p, i64, p, p],
         "ck_act_rotate_f32": [p, i64, i64, i64, i32, i32, p, p],
         "ck_probe_mfma_i8": [p, i64, i32, p, p],
@@ -133,6 +145,12 @@ def bind(path: str) -> ctypes.CDLL:
     L.ck_swiglu_mlp_workspace_size.restype = sz
     L.ck_cross_attn_workspace_size.argtypes = [i64] * 7
     L.ck_cross_attn_workspace_size.restype = sz
+    for f in (L.ck_mx4_gemm_workspace_size, L.ck_mx4_linear_workspace_size):
+        f.argtypes = [i64, i64, i64]
+        f.restype = sz
+    for f in (L.ck_mx4_rows, L.ck_mx4_cols):
+        f.argtypes = [i64]
+        f.restype = i64
     L.ck_probe_mfma_workgroups.argtypes = []
     L.ck_probe_mfma_workgroups.restype = i64
     L.ck_noalloc_scratch_bytes.argtypes = []
@@ -686,7 +704,9 @@ def _native():
             raise ImportError(f"{os.path.join(HERE, '_marshal.so')} is missing or does not load ({e}): build it "
                               "with `python -m swiglu_mlp_amd.build`") from e
         m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
-                 for f in (L.ck_qk_norm_rope, L.ck_cross_attn, L.ck_cross_attn_workspace_size)),
+                 for f in (L.ck_qk_norm_rope, L.ck_cross_attn, L.ck_cross_attn_workspace_size, L.ck_mx4_weight_prep,
+                           L.ck_mx4_act_quant, L.ck_mx4_dequant, L.ck_mx4_gemm_bf16, L.ck_mx4_gemm_workspace_size,
+                           L.ck_mx4_linear, L.ck_mx4_linear_workspace_size, L.ck_block_norm)),
                torch._C._cuda_getCurrentRawStream)
         _calls = m
     return _calls
@@ -742,6 +762,107 @@ def ck_cross_attn(q, k, v, scale=None, kv_len=None, key_mask=None, out=None, wor
     return _done("ck_cross_attn", (_calls or _native()).cross_attn(q, k, v, scale, kv_len, key_mask, out, workspace))
 
 
+# ---------------------------------------------------------------------------
+# MX FP4 linears: microscaled 4-bit weights and activations
+# ---------------------------------------------------------------------------
+def ck_mx4_weight_prep(w, group: int = 128, layout="blocked"):
+    """Rotate and quantize an FP32 weight [n, k] -> (codes, scales), uint8.
+    layout "blocked" (default, what the linear reads): codes [n / 32, k / 64,
+    1024] and scales [n / 32, k / 256, 256], n padded to 32 and k to 256;
+    "rows" (serialized): codes [n, k / 2], the even k in the low nibble, and
+    scales [n, k / 32].  group 1: no rotation."""
+    return _done("ck_mx4_weight_prep", (_calls or _native()).mx4_quant(w, CK_ACT_NONE, group, None, _layout_code(layout),
+                                                                      True))
+
+
+def ck_mx4_weight_pack(codes, scales):
+    """Serialized codes [n, k / 2] and E8M0 scales [n, k / 32] (uint8, row-major)
+    -> (codes, scales) in the blocked layout."""
+    import torch
+    _need(codes, torch.uint8, 2, "codes")
+    _need(scales, torch.uint8, 2, "scales")
+    n, k = codes.shape[0], 2 * codes.shape[1]
+    if tuple(scales.shape) != (n, k // 32) or scales.device != codes.device:
+        raise ValueError(f"scales need shape ({n}, {k // 32}) on {codes.device}, got {tuple(scales.shape)} on "
+                         f"{scales.device}")
+    if k < 64 or k % 64 or k > 32768:
+        raise ValueError(f"in_features must be a multiple of 64 up to 32768, got {k}")
+    rb, kp = (n + 31) // 32, (k + 255) // 256 * 256
+    with torch.cuda.device(codes.device):
+        out = torch.empty((rb, kp // 64, 1024), dtype=torch.uint8, device=codes.device)
+        out_scales = torch.empty((rb, kp // 256, 256), dtype=torch.uint8, device=codes.device)
+        _call("ck_mx4_weight_pack", codes.data_ptr(), scales.data_ptr(), n, k, out.data_ptr(), out_scales.data_ptr(),
+              _stream(codes))
+    return out, out_scales
+
+
+def ck_mx4_act_quant(x, input_act=None, group: int = 128, k: int | None = None, layout="blocked"):
+    """Rotate and quantize a BF16 activation [m, columns] (silu(gate) * up of
+    [gate | up] with input_act="swiglu") -> (codes, scales) as
+    ck_mx4_weight_prep.  The rows may be strided."""
+    return _done("ck_mx4_act_quant", (_calls or _native()).mx4_quant(x, _act_code(input_act), group, k,
+                                                                    _layout_code(layout), False))
+
+
+def ck_mx4_dequant(codes, scales, rows: int | None = None, k: int | None = None):
+    """The values that codes and scales stand for, BF16 [rows, k] (exact).
+    rows and k: the logical sizes of blocked operands (default: with padding)."""
+    return _done("ck_mx4_dequant", (_calls or _native()).mx4_dequant(codes, scales, rows, k))
+
+
+def ck_mx4_gemm_bf16(x_codes, x_scales, w_codes, w_scales, m: int, n: int | None = None, out=None, workspace=None,
+                     bias=None, residual=None):
+    """y = bf16(x w^T (+ bias) (+ residual)) of blocked 4-bit operands with m and
+    n logical rows (n default: the weight's padded rows)."""
+    return _done("ck_mx4_gemm_bf16", (_calls or _native()).mx4_gemm(x_codes, x_scales, w_codes, w_scales, m, n, bias,
+                                                                   residual, out, workspace))
+
+
+def ck_mx4_linear(x, w_codes, w_scales, n: int | None = None, group: int = 128, input_act=None, out=None,
+                  workspace=None, bias=None, residual=None):
+    """The linear on a 4-bit weight: rotate and quantize x (BF16 [m, k], or
+    [m, 2 k] with input_act="swiglu"; rows may be strided), multiply, add the FP32
+    bias [n] and the BF16 residual [m, n].
+
+    (w_codes, w_scales) from ck_mx4_weight_prep or ck_mx4_weight_pack, rotated by
+    the same group; n: its out_features when not a multiple of 32.  `out` may be
+    the residual itself and shares no memory with anything else; nor does
+    `workspace` (uint8, 256-byte aligned, ck_mx4_linear_workspace_size(m, k, n)
+    bytes)."""
+    return _done("ck_mx4_linear", (_calls or _native()).mx4_linear(x, w_codes, w_scales, n, group,
+                                                                  _act_code(input_act), bias, residual, out, workspace))
+
+
+# ---------------------------------------------------------------------------
+# Between two sub-blocks: residual sum, gate and norms
+# ---------------------------------------------------------------------------
+CK_DTYPE_FP32 = 2
+CK_NORM_NONE, CK_NORM_RMS, CK_NORM_LAYER = 0, 1, 2
+_NORM = {None: CK_NORM_NONE, "none": CK_NORM_NONE, "rms": CK_NORM_RMS, "layer": CK_NORM_LAYER}
+
+
+def ck_block_norm(x, branch=None, gate=None, residual_scale: float = 1.0, branch_scale: float = 1.0, branch_norm=None,
+                  branch_weight=None, branch_bias=None, norm="rms", weight=None, bias=None, scale=None, shift=None,
+                  eps: float = 1e-6, x_out=None, out=None):
+    """What joins two sub-blocks, in one launch:
+
+        r = residual_scale x + branch_scale gate branch_norm(branch)
+        h = norm(r) (1 + scale) + shift
+
+    x, branch: BF16 or FP16 [batch, tokens, width] or [tokens, width], rows may be
+    strided.  Norms "rms", "layer" or None, with FP32 weights and biases [width].
+    gate, scale, shift: of x's type or all FP32; [width], [batch, width] (a column
+    range of a packed modulation, say) or x's shape.  h is computed from the
+    unrounded r.  Outputs are new contiguous tensors, or x_out / out, which may be
+    x or branch themselves and share no memory with anything else of the call.
+    Returns (r, h); h alone without a branch, r alone with norm=None."""
+    if branch_norm not in _NORM or norm not in _NORM:
+        raise ValueError(f"unknown norm {branch_norm if branch_norm not in _NORM else norm!r}")
+    return _done("ck_block_norm", (_calls or _native()).block_norm(
+        x, branch, gate, residual_scale, branch_scale, _NORM[branch_norm], branch_weight, branch_bias, _NORM[norm], weight,
+        bias, scale, shift, eps, x_out, out))
+
+
 def ck_silu_f32(gate):
     import torch
     if gate.dtype != torch.bfloat16 or gate.device.type != "cuda" or not gate.is_contiguous():
@@ -773,3 +894,5 @@ int8_gemm_bf16 = ck_int8_gemm_bf16
 swiglu_mlp = ck_swiglu_mlp
 qk_norm_rope = ck_qk_norm_rope
 cross_attn = ck_cross_attn
+mx4_linear = ck_mx4_linear
+block_norm = ck_block_norm

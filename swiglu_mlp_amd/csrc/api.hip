@@ -1,6 +1,7 @@
 // api.hip -- the C ABI declared in include/ck.h: host-side argument checks,
 // workspace carving and kernel dispatch.  No function here allocates, frees or
 // synchronises; all checks complete before anything is enqueued.
+#include "api_checks.hpp"
 #include "ck.h"
 #include "ck_internal.hpp"
 
@@ -10,33 +11,7 @@
 
 namespace {
 
-constexpr size_t kAlign = 256;
-
-size_t round_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-bool pow2_group(int32_t g) { return g >= 1 && g <= 256 && (g & (g - 1)) == 0; }
-
-// Checks shared by every call that takes an in_features dimension.
-ck_status check_k(int64_t k, int32_t group)
-{
-    if (!pow2_group(group)) return CK_EUNSUPPORTED;
-    if (k < 1) return CK_ESHAPE;
-    if (k > CK_MAX_K) return CK_EUNSUPPORTED;
-    if (k % 64 != 0 || k % group != 0) return CK_ESHAPE;
-    return CK_OK;
-}
-
-ck_status check_act(int32_t act, int64_t ldx, int64_t k)
-{
-    if (act != CK_ACT_NONE && act != CK_ACT_SWIGLU) return CK_EINVAL;
-    const int64_t need = act == CK_ACT_SWIGLU ? 2 * k : k;
-    if (ldx < need || ldx % 8 != 0) return CK_ESHAPE;
-    return CK_OK;
-}
-
-ck_status from_hip(hipError_t e) { return e == hipSuccess ? CK_OK : CK_EHIP; }
+using namespace ck::api;
 
 int64_t pad_rows(int64_t r) { return (r + 255) / 256 * 256; }
 
@@ -67,12 +42,6 @@ ck_status check_gemm_extent(int64_t m, int64_t n, int64_t k)
         return CK_EUNSUPPORTED;
     return CK_OK;
 }
-
-#define CK_TRY(expr)                     \
-    do {                                 \
-        const ck_status st_ = (expr);    \
-        if (st_ != CK_OK) return st_;    \
-    } while (0)
 
 // Scratch of ck_int8_linear_noalloc: the activation codes and row scales of
 // one call, in device memory the library holds itself (each GPU gets its own
@@ -580,16 +549,7 @@ static ck_status check_heads(const ck_heads& h)
     return CK_OK;
 }
 
-// a * b * c of non-negative sizes, or limit if it is not below it.
-static int64_t product_below(int64_t a, int64_t b, int64_t c, int64_t limit)
-{
-    if (a == 0 || b == 0 || c == 0) return 0;
-    if (a >= limit || b >= limit || c >= limit || a * b >= limit) return limit;
-    return a * b * c < limit ? a * b * c : limit;
-}
-
 // Sizes whose launches stay below 2^32 threads in a grid.
-constexpr int64_t kMaxIndex = 0x7fffffffLL;   // a dimension alone
 constexpr int64_t kMaxNormHeads = 1 << 25;    // batch * tokens * heads of a side of the norm (32 lanes each)
 constexpr int64_t kMaxAttnRows = 1 << 30;     // batch * tq * heads
 constexpr int64_t kMaxKeyHeads = 1 << 22;     // kv_batch * kv_heads

@@ -150,6 +150,42 @@ size_t cross_attn_workspace(int64_t batch, int64_t kv_batch, int64_t tq, int64_t
                             int64_t kv_heads, int64_t d);
 hipError_t launch_cross_attn(const AttnArgs& a, hipStream_t st);
 
+// Microscaled 4-bit operands (mx4_quant.hip): kind as launch_quant_rows; codes
+// and scales row-major or blocked (mx4.hpp).
+hipError_t launch_mx4_quant(int kind, const void* src, int64_t ld, int64_t m, int64_t k, int g, bool blocked,
+                            uint8_t* codes, uint8_t* scales, hipStream_t st);
+hipError_t launch_mx4_pack(const uint8_t* codes, const uint8_t* scales, int64_t n, int64_t k, uint8_t* out,
+                           uint8_t* out_scales, hipStream_t st);
+hipError_t launch_mx4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t m, int64_t k, bool blocked,
+                              uint16_t* out, hipStream_t st);
+
+// y = bf16(x . w^T (+ bias) (+ residual)) of blocked 4-bit operands
+// (mx4_gemm.hip); workspace of mx4_gemm_workspace bytes (0: unused).
+size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k);
+hipError_t launch_mx4_gemm(const uint8_t* xc, const uint8_t* xs, const uint8_t* wc, const uint8_t* ws, int64_t m,
+                           int64_t n, int64_t k, uint16_t* y, EpiExtra ex, void* workspace, hipStream_t st);
+
+// Residual sum with the branch's norm and gate, and the next norm with its
+// modulation (block_norm.hip).  Strides in elements; null pointers: absent.
+struct ModArgs {
+    const void* p;
+    int64_t sb, st;
+};
+struct BlockNormArgs {
+    const uint16_t* x;
+    const uint16_t* branch;
+    uint16_t* x_out;
+    uint16_t* out;
+    int64_t x_sb, x_st, b_sb, b_st, xo_sb, xo_st, o_sb, o_st;
+    int64_t batch, tokens, width;
+    ModArgs gate, scale, shift;
+    const float *bw, *bb, *w, *b;
+    int branch_kind, kind;   // 0 none, 1 RMS, 2 layer
+    bool mod32, fp16;
+    float residual_scale, branch_scale, eps;
+};
+hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t st);
+
 // Measurement kernels (probe.hip): the INT8 MFMA loop on one workgroup per CU
 // (optionally reading 0.5 KB of LDS per MFMA), and a row stream with a given
 // read / write byte count per row.
