@@ -454,7 +454,8 @@ size_t ck_cross_attn_workspace_size(int64_t batch, int64_t kv_batch, int64_t tq,
  * Padding columns hold zero products; padding rows are never read into valid
  * outputs (an activation's are not written).
  * Shapes as in the INT8 calls (k % 64 == 0, k % group == 0, n % 16 == 0,
- * k <= CK_MAX_K), with rp * kp < 2^34 for either operand and m n < 2^35. */
+ * k <= CK_MAX_K), with rp * kp < 2^34 for either operand, n < 2^21 and
+ * m n < 2^35. */
 int64_t ck_mx4_rows(int64_t rows);   /* rp (0 for rows <= 0) */
 int64_t ck_mx4_cols(int64_t k);      /* kp (0 for k <= 0) */
 

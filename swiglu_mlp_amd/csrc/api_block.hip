@@ -12,6 +12,7 @@ namespace {
 
 constexpr int64_t kMaxValues = 1LL << 34;     // of an operand, padded: launches below 2^32 threads
 constexpr int64_t kMaxOutputs = 1LL << 35;    // m * n
+constexpr int64_t kMaxFeatures = 1LL << 21;   // 256 rows of FP32 sums in 32-bit offsets
 
 size_t codes_bytes(int64_t rows, int64_t k) { return (size_t)(ck::mx4::pad_rows(rows) * ck::mx4::pad_cols(k) / 2); }
 size_t scales_bytes(int64_t rows, int64_t k) { return (size_t)(ck::mx4::pad_rows(rows) * ck::mx4::pad_cols(k) / 32); }
@@ -36,7 +37,7 @@ ck_status check_product(int64_t m, int64_t n, int64_t k, int32_t group)
     CK_TRY(check_operand(m, k, group));
     CK_TRY(check_operand(n, k, group));
     if (n % 16 != 0) return CK_ESHAPE;
-    if (m > 0 && n >= kMaxOutputs / m) return CK_EUNSUPPORTED;
+    if (n >= kMaxFeatures || (m > 0 && n >= kMaxOutputs / m)) return CK_EUNSUPPORTED;
     return CK_OK;
 }
 
