@@ -10,27 +10,34 @@
 //
 // The matrix cores set the pace of large products: random codes reach 6.5 of
 // the nominal 10 PFLOP/s in a loop of nothing but these instructions (the clock
-// falls under their power).  So the kernel keeps them fed:
-//  * A workgroup of 4 waves (2 x 2) owns a BM x BN tile; a wave's part is FM x FN
+// falls under their power).  A wave issues a product every 32 cycles and some 4
+// other instructions in its shadow; past that each one more costs 4 to 8 cycles
+// (measured: 36 cycles a product alone or with 2 scalar ones, 57 with 6, 73 with
+// 8).  So the kernel is built for few instructions a product:
+//  * A group of 4 waves (2 x 2) owns a BM x BN tile; a wave's part is FM x FN
 //    fragments of 32 x 32, accumulated in AGPRs.  It reads FM + FN blocks from
 //    LDS for FM FN products.
-//  * K advances 2 KSL slices a stage; stages go through a ring of LDS slots by
-//    DMA (buffer_load ... lds), P of them ahead.  A stage is two halves around
-//    one barrier: each multiplies KSL slices while it reads the other half's
-//    fragments, so products never wait for LDS.  Reads and loads are placed
-//    between the products in source order.
-//  * Scales come with the codes: 256 bytes for 32 rows and 256 k (4 slices), one
-//    DMA instruction a wave, read as one register a fragment for 4 slices.
-//  * Workgroups stay and take tiles in turn; the stages run on from a tile to the
-//    next, whose loads so overlap the epilogue.  The workgroups of an XCD take
-//    consecutive tiles and share operands in its L2.
-//  * Few tiles: k is split over several workgroups, which write FP32 partial sums
-//    that a second kernel adds in a fixed order.
+//  * K advances two slices (128 values) a stage.  Stages go through a ring of 4
+//    LDS slots by DMA (buffer_load ... lds, two for one LDS address), 3 ahead.  A
+//    stage is two halves around one barrier: each multiplies one slice while it
+//    reads the next one's fragments, so products never wait for LDS.  Reads and
+//    loads are placed between the products in source order.
+//  * Two stages make a pair: 256 values, one chunk of scales (256 bytes for 32
+//    rows; one DMA instruction a wave, one register a fragment).  Slots, scale
+//    selects and the ends of units are constants of a stage's place in its pair.
+//  * 256 x 256 tiles, one group a CU: workgroups stay and take tiles in turn; the
+//    stages run on from a tile to the next, whose loads so overlap the epilogue.
+//    The workgroups of an XCD take consecutive tiles and share operands in its L2.
+//  * Smaller tiles, several groups a workgroup, each with a range of k: their
+//    waves fill each other's gaps, and their sums meet in LDS.
+//  * Few tiles: k is split over several workgroups too, which write FP32 partial
+//    sums that a second kernel adds in a fixed order.
 #include "ck_internal.hpp"
 #include "mx4.hpp"
 
 #include <algorithm>
 #include <type_traits>
+#include <utility>
 
 namespace ck {
 namespace mx4 {
@@ -58,20 +65,32 @@ __device__ __forceinline__ void workgroup_barrier()
     asm volatile("" ::: "memory");
 }
 
-// 16 bytes a lane from memory to LDS address lds + 16 lane, not tracked by the
-// compiler (which would wait for all of them before any LDS read): the waits are
-// counted by hand.
-__device__ __forceinline__ void lds_dma_b128(v4i rsrc, uint32_t voff, uint32_t soff, uint32_t lds)
+// 16 bytes a lane from memory to LDS, not tracked by the compiler (which would
+// wait for all of them before any LDS read): the waits are counted by hand.  Lane
+// l's bytes land at lds + OFF + 16 l.  TWO: and those 1 KB on at 1 KB on (the
+// instruction's offset counts in memory and in LDS).
+template <int OFF, bool TWO>
+__device__ __forceinline__ void lds_dma(v4i rsrc, uint32_t voff, uint32_t soff, uint32_t lds)
 {
-    asm volatile(
-        "s_mov_b32 m0, %3\n\t"
-        "s_nop 0\n\t"
-        "buffer_load_dwordx4 %0, %1, %2 offen lds"
-        :
-        : "v"(voff), "s"(rsrc), "s"(soff), "s"(lds)
-        : "memory", "m0");
+    if constexpr (TWO)
+        asm volatile(
+            "s_add_u32 m0, %3, %4\n\t"
+            "s_nop 0\n\t"
+            "buffer_load_dwordx4 %0, %1, %2 offen lds\n\t"
+            "buffer_load_dwordx4 %0, %1, %2 offen offset:1024 lds"
+            :
+            : "v"(voff), "s"(rsrc), "s"(soff), "s"(lds), "n"(OFF)
+            : "memory", "m0", "scc");
+    else
+        asm volatile(
+            "s_add_u32 m0, %3, %4\n\t"
+            "s_nop 0\n\t"
+            "buffer_load_dwordx4 %0, %1, %2 offen lds"
+            :
+            : "v"(voff), "s"(rsrc), "s"(soff), "s"(lds), "n"(OFF)
+            : "memory", "m0", "scc");
 }
-__device__ __forceinline__ void lds_dma_b128(const uint8_t* at, uint32_t lds)
+__device__ __forceinline__ void lds_dma(const uint8_t* at, uint32_t lds)
 {
     asm volatile(
         "s_mov_b32 m0, %1\n\t"
@@ -97,20 +116,30 @@ __device__ __forceinline__ v16f product(v4i a, v4i b, v16f c, int sa, int sb)
                                                            sb);
 }
 
-template <int BM_, int BN_, int KSL_>
+// f(0), f(1), ... f(N - 1) with constants as arguments.
+template <typename F, int... I>
+__device__ __forceinline__ void for_each_in(F&& f, std::integer_sequence<int, I...>)
+{
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void for_each(F&& f)
+{
+    for_each_in(f, std::make_integer_sequence<int, N>{});
+}
+
+template <int BM_, int BN_, int GROUPS_>
 struct Cfg {
-    static constexpr int BM = BM_, BN = BN_, KSL = KSL_;
-    static constexpr int KS2 = 2 * KSL;                 // slices a stage
+    static constexpr int BM = BM_, BN = BN_, GROUPS = GROUPS_;
     static constexpr int FM = BM / 64, FN = BN / 64;    // a wave's fragments
-    static constexpr int A_BLK = (BN / 32) * KS2, B_BLK = (BM / 32) * KS2;
-    static constexpr int AW = A_BLK / 4, XW = B_BLK / 4, L = AW + XW;   // blocks a wave loads for a stage
+    static constexpr int A_BLK = BN / 16, B_BLK = BM / 16;              // 1 KB blocks of a stage
+    static constexpr int AW = A_BLK / 4, XW = B_BLK / 4, L = AW + XW;   // a wave's share
+    static constexpr int AP = (AW + 1) / 2, XP = (XW + 1) / 2;          // as loads of one row block: both slices, or one
     static constexpr int CODES = (A_BLK + B_BLK) * 1024;
     static constexpr int CHUNKS = (BM + BN) / 32;       // of scales (32 rows, 256 k)
     static constexpr int CPW = (CHUNKS + 3) / 4;        // chunks a wave loads, into its own KB
-    static constexpr int NBUF = 4, P = NBUF - 1;
-    static constexpr int SBUF = KSL == 1 ? 2 : NBUF;    // a slot of scales lasts 4 slices
-    static constexpr int LDS = NBUF * CODES + SBUF * 4096;
-    static_assert(KSL == 1 || KSL == 2, "a stage is half of a scale chunk's k, or all of it");
+    static constexpr int RING = 4 * CODES + 2 * 4096;   // 4 slots of codes, 2 of scales
+    static constexpr int LDS = GROUPS * RING;
     static_assert(LDS <= 160 * 1024, "LDS");
     static_assert(A_BLK % 4 == 0 && B_BLK % 4 == 0, "blocks split evenly over 4 waves");
 };
@@ -123,7 +152,7 @@ struct Args {
     int kb;             // 1 KB blocks (slices) of a 32-row block: kp / 64
     int xb, wb;         // 32-row blocks of x and w
     int tiles_m, tiles_n, group_m;
-    int splits, stages; // stages of one unit (a tile and one of the splits of k)
+    int splits;
 };
 
 // Tile j of the grouped order -> (tm, tn): columns of `group_m` tile-rows.
@@ -138,36 +167,33 @@ __device__ __forceinline__ void tile_coords(int j, int tiles_m, int tiles_n, int
 }
 
 // PART: FP32 partial sums out.  EXTRA: bias and / or residual.
-template <int BM, int BN, int KSL, bool PART, bool EXTRA>
-__global__ __launch_bounds__(256) void mx4_gemm_kernel(Args g)
+template <int BM, int BN, int GROUPS, bool PART, bool EXTRA>
+__global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
 {
     // The body uses AMDGPU-only types; the host pass only needs the launch stub.
 #if defined(__HIP_DEVICE_COMPILE__)
-    using C = Cfg<BM, BN, KSL>;
+    using C = Cfg<BM, BN, GROUPS>;
     __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
     constexpr int NMF = C::FN * C::FM;                  // products of a slice
     constexpr int NDS = C::FN + C::FM;                  // fragment reads of a slice
-    // Large tiles spread a stage's loads over both halves: a burst of them fills
-    // the address unit's queue and holds up the products behind it.
-    constexpr bool SPREAD = KSL == 1;
-    constexpr int HL = SPREAD ? C::L / 2 : C::L;        // loads of the first half
+    constexpr int NPAIR = C::AP + C::XP;                // loads (of one or two KB) of a stage
+    constexpr int H0 = NPAIR / 2;                       // of them, in the first half
+    constexpr int L0 = (H0 < C::AP ? H0 : C::AP) * (C::AW > 1 ? 2 : 1) +
+                       (H0 > C::AP ? H0 - C::AP : 0) * (C::XW > 1 ? 2 : 1);   // as instructions
     constexpr int NST = PART ? 0 : 2 * NMF;             // stores of an epilogue (PART: too many to count, waited for)
     // Loads issued after the last of stage s + 1 at the middle of stage s: those of
-    // the stages up to s + P but for the second half's, with their scales (KSL 1:
-    // one of any two consecutive stages has some).
-    constexpr int OUTS = SPREAD ? (C::P - 2) * C::L + HL + 1 : (C::P - 1) * (C::L + 1);
-    static_assert(!SPREAD || C::P == 3, "the count above");
+    // s + 2, the first half's of s + 3, and the scales with one of the two.
+    constexpr int OUTS = C::L + L0 + 1;
     static_assert(OUTS + NST < 64, "vmcnt range");
 
-    const int tid = threadIdx.x;
-    const int lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & 3);
+    const int group = GROUPS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) : 0;
     const int G = gridDim.x, b = blockIdx.x;
     const int tiles = g.tiles_m * g.tiles_n;
-    const int units = tiles * g.splits;                 // split-major
-    const int KT = g.stages;
-    const int my_units = (units - b + G - 1) / G;
-    const int total = my_units * KT;
+    const int units = tiles * g.splits;                 // a tile and one of the splits of k, split-major
+    const int my_units = (units - b + G - 1) / G;       // more than one only with one group and one split
+    const int all_pairs = g.kb / 4, ranges = g.splits * GROUPS;
 
     // Within a full round the workgroups of one XCD (b % 8) take consecutive units.
     const bool xcd_order = (G & 7) == 0;
@@ -176,157 +202,170 @@ __global__ __launch_bounds__(256) void mx4_gemm_kernel(Args g)
         const bool full = xcd_order & ((q + 1) * G <= units);
         return q * G + (full ? b_xcd : b);
     };
-    const uint32_t smem_addr = (uint32_t)(uintptr_t)(lds_void_t*)smem;
+    // this group's range of pairs (at least one: there are no more ranges than pairs)
+    const int range = (GROUPS > 1 || PART) ? (unit_of(0) / tiles) * GROUPS + group : 0;
+    const int pair0 = (int)((int64_t)range * all_pairs / ranges);
+    const int pairs = (int)((int64_t)(range + 1) * all_pairs / ranges) - pair0;
+    const int most_pairs = (all_pairs + ranges - 1) / ranges;
+    const uint32_t ring = (uint32_t)(uintptr_t)(lds_void_t*)smem + (uint32_t)(group * C::RING);
     const uint32_t lane16 = (uint32_t)lane * 16u;
 
-    // ---- the load cursor: the stage to be loaded next (it stays at the last one,
-    // whose repeated loads go to slots that nobody reads again, so that the number
-    // of loads of a stage is constant) ----
-    int ls = 0, lq = 0, lkt = 0;
-    v4i rs_w, rs_x;                                     // the tile's rows of codes, from the unit's first slice
-    const uint8_t* sp;                                  // this lane's scales of the unit's first 256 k
+    // ---- the load cursor: the stage to be loaded next.  After the last unit it
+    // starts over on it: those loads go to slots that nobody reads again, and the
+    // number of loads of a stage stays constant. ----
+    int lq = 0, lpairs = pairs;
+    v4i rs_w, rs_x;                                     // the tile's rows of codes
+    uint32_t so_w[C::AP], so_x[C::XP];                  // where in them this wave's loads of the stage are
+    const uint8_t* sp;                                  // this lane's scales of the pair
     auto set_unit = [&](int q) {
-        const int u = unit_of(q), k0 = (u / tiles) * KT * C::KS2;
+        const int u = unit_of(q);
         int tm, tn;
         tile_coords(u % tiles, g.tiles_m, g.tiles_n, g.group_m, tm, tn);
         const int64_t wb0 = (int64_t)tn * (BN / 32), xb0 = (int64_t)tm * (BM / 32);
-        const int64_t w0 = (wb0 * g.kb + k0) * 1024, x0 = (xb0 * g.kb + k0) * 1024;
+        const int64_t w0 = wb0 * g.kb * 1024, x0 = xb0 * g.kb * 1024;
         // blocks past the operand's end are outside the buffer and read as zero
         rs_w = make_rsrc(g.wc + w0, (int64_t)g.wb * g.kb * 1024 - w0);
         rs_x = make_rsrc(g.xc + x0, (int64_t)g.xb * g.kb * 1024 - x0);
+        // block ai of a stage: row block ai / 2, slice ai % 2
+#pragma unroll
+        for (int p = 0; p < C::AP; ++p) {
+            const int ai = wave * C::AW + 2 * p;
+            so_w[p] = (uint32_t)((ai / 2) * g.kb + ai % 2 + pair0 * 4) * 1024u;
+        }
+#pragma unroll
+        for (int p = 0; p < C::XP; ++p) {
+            const int ai = wave * C::XW + 2 * p;
+            so_x[p] = (uint32_t)((ai / 2) * g.kb + ai % 2 + pair0 * 4) * 1024u;
+        }
         // a chunk past the end takes the last block's scales (for products that are not stored)
         const int c = min(wave * C::CPW + min(lane >> 4, C::CPW - 1), C::CHUNKS - 1);
         const bool w = c < BN / 32;
         const int64_t rb = w ? min((int64_t)g.wb - 1, wb0 + c) : min((int64_t)g.xb - 1, xb0 + c - BN / 32);
-        sp = (w ? g.ws : g.xs) + (rb * (g.kb / 4) + k0 / 4) * 256 + (lane & 15) * 16;
+        sp = (w ? g.ws : g.xs) + (rb * (g.kb / 4) + pair0) * 256 + (lane & 15) * 16;
     };
-    auto advance = [&]() {
-        if (ls + 1 < total) {
-            ++ls;
-            if (++lkt == KT) {
-                lkt = 0;
-                set_unit(++lq);
-            }
-        }
-    };
-    // Block a of this wave's share of a stage: block ai covers row block ai / KS2, slice ai % KS2.
-    auto issue_one = [&](int a, uint32_t slot) {
-        const bool w = a < C::AW;
-        const int ai = w ? wave * C::AW + a : wave * C::XW + (a - C::AW);
-        const uint32_t off = (uint32_t)(lkt * C::KS2 + (ai / (unsigned)C::KS2) * g.kb + (ai % (unsigned)C::KS2)) * 1024u;
-        if (w)
-            lds_dma_b128(rs_w, lane16, off, slot + (uint32_t)ai * 1024u);
+    // Load p of a stage into the slot whose share of this wave begins at LDS address `at`.
+    auto issue = [&](auto p_, uint32_t at) {
+        constexpr int p = decltype(p_)::value;
+        if constexpr (p < C::AP)
+            lds_dma<p * 2048, (C::AW > 1)>(rs_w, lane16, so_w[p], at + (uint32_t)(wave * C::AW * 1024));
         else
-            lds_dma_b128(rs_x, lane16, off, slot + (uint32_t)(C::A_BLK + ai) * 1024u);
+            lds_dma<C::A_BLK * 1024 + (p - C::AP) * 2048, (C::XW > 1)>(rs_x, lane16, so_x[p - C::AP],
+                                                                     at + (uint32_t)(wave * C::XW * 1024));
     };
-    auto issue_scales = [&](int d) {   // d: counts the slots of scales
-        lds_dma_b128(sp + (lkt * C::KS2 / 4) * 256,
-                     smem_addr + (uint32_t)(C::NBUF * C::CODES + (d % C::SBUF) * 4096 + wave * 1024));
+    auto issue_scales = [&](uint32_t slot) {
+        lds_dma(sp, ring + 4 * C::CODES + slot * 4096 + (uint32_t)wave * 1024);
+        sp += 256;
+    };
+    auto next_stage = [&]() {
+#pragma unroll
+        for (int p = 0; p < C::AP; ++p) so_w[p] += 2048;
+#pragma unroll
+        for (int p = 0; p < C::XP; ++p) so_x[p] += 2048;
+    };
+    auto next_pair = [&]() {   // after an odd stage
+        if (--lpairs == 0) {
+            asm volatile("" ::: "memory");   // a branch, not its ~100 scalar operations in every pair
+            lpairs = pairs;
+            lq = min(lq + 1, my_units - 1);
+            set_unit(lq);
+        }
     };
 
     v16f acc[C::FN][C::FM];
     const int lr = lane & 31, lh = lane >> 5;
     const int wm0 = (wave & 1) * (BM / 2), wn0 = (wave >> 1) * (BN / 2);
-    auto frag_a = [&](int buf, int i, int ks) {
-        return *reinterpret_cast<const v4i*>(smem + buf * C::CODES + (((wn0 >> 5) + i) * C::KS2 + ks) * 1024 + lane * 16);
-    };
-    auto frag_b = [&](int buf, int j, int ks) {
-        return *reinterpret_cast<const v4i*>(smem + buf * C::CODES + (C::A_BLK + ((wm0 >> 5) + j) * C::KS2 + ks) * 1024 +
-                                             lane * 16);
-    };
-    auto scale = [&](int d, int c) {
-        return *reinterpret_cast<const int*>(smem + C::NBUF * C::CODES + (d % C::SBUF) * 4096 + (c / C::CPW) * 1024 +
-                                             (c % C::CPW) * 256 + lane * 4);
+    // this lane's places in the pair's first slot (they change sides after every pair)
+    const char* pa = smem + group * C::RING + (wn0 / 32) * 2048 + lane * 16;
+    const char* pb = smem + group * C::RING + C::A_BLK * 1024 + (wm0 / 32) * 2048 + lane * 16;
+    const char* const ps = smem + group * C::RING + 4 * C::CODES + lane * 4;
+    int side = 2 * C::CODES;
+    uint32_t cur = 0;                                   // the pair's side: 0 or 1
+    auto frag_a = [&](int off, int i) { return *reinterpret_cast<const v4i*>(pa + off + i * 2048); };
+    auto frag_b = [&](int off, int j) { return *reinterpret_cast<const v4i*>(pb + off + j * 2048); };
+    auto scale = [&](uint32_t slot, int c) {
+        return *reinterpret_cast<const int*>(ps + slot * 4096 + (c / C::CPW) * 1024 + (c % C::CPW) * 256);
     };
 
     set_unit(0);
 #pragma unroll
-    for (int p = 0; p < C::P; ++p) {
-        if (KSL == 2 || p % 2 == 0) issue_scales(KSL == 2 ? p : p / 2);
-#pragma unroll
-        for (int a = 0; a < C::L; ++a) issue_one(a, smem_addr + (uint32_t)(p * C::CODES));
-        advance();
+    for (int p = 0; p < 3; ++p) {
+        if (p % 2 == 0) issue_scales(p / 2);
+        for_each<NPAIR>([&](auto i) { issue(i, ring + (uint32_t)(p * C::CODES)); });
+        next_stage();
+        if (p % 2 == 1) next_pair();
     }
-    wait_vmcnt<(C::P - 1) * C::L + (KSL == 2 ? C::P - 1 : 1)>();
+    wait_vmcnt<2 * C::L + 1>();
     workgroup_barrier();
-    v4i fa[KSL][C::FN], fb[KSL][C::FM], ga[KSL][C::FN], gb[KSL][C::FM];
-    int sa[C::FN], sb[C::FM], na[C::FN], nb[C::FM];     // scales of 4 slices, and the next ones
+    v4i fa[C::FN], fb[C::FM], ga[C::FN], gb[C::FM];
+    int sa[C::FN], sb[C::FM], na[C::FN], nb[C::FM];     // the pair's scales, and the next one's
 #pragma unroll
-    for (int ks = 0; ks < KSL; ++ks) {
+    for (int i = 0; i < C::FN; ++i) fa[i] = frag_a(0, i), sa[i] = scale(0, (wn0 >> 5) + i);
 #pragma unroll
-        for (int i = 0; i < C::FN; ++i) fa[ks][i] = frag_a(0, i, ks);
-#pragma unroll
-        for (int j = 0; j < C::FM; ++j) fb[ks][j] = frag_b(0, j, ks);
-    }
-#pragma unroll
-    for (int i = 0; i < C::FN; ++i) sa[i] = scale(0, (wn0 >> 5) + i);
-#pragma unroll
-    for (int j = 0; j < C::FM; ++j) sb[j] = scale(0, BN / 32 + (wm0 >> 5) + j);
+    for (int j = 0; j < C::FM; ++j) fb[j] = frag_b(0, j), sb[j] = scale(0, BN / 32 + (wm0 >> 5) + j);
 
-    // Product k of a half whose first slice is slice Q0 of the scales' four.
-    auto mfma_step = [&](int k, auto q0, const v4i (&w)[KSL][C::FN], const v4i (&x)[KSL][C::FM], bool zero) {
-        constexpr int Q0 = decltype(q0)::value;
-        const int ks = k / NMF, i = (k % NMF) / C::FM, j = (k % NMF) % C::FM;
-        const v16f c = (zero && ks == 0) ? v16f{} : acc[i][j];
-        if (ks == 0)
-            acc[i][j] = product<Q0>(w[0][i], x[0][j], c, sa[i], sb[j]);
-        else
-            acc[i][j] = product<(Q0 + 1) & 3>(w[KSL - 1][i], x[KSL - 1][j], c, sa[i], sb[j]);
+    // Product k of a slice, slice Q of the pair.
+    auto mfma_step = [&](int k, auto q, const v4i (&w)[C::FN], const v4i (&x)[C::FM], bool zero) {
+        const int i = k / C::FM, j = k % C::FM;
+        const v16f c = zero ? v16f{} : acc[i][j];
+        acc[i][j] = product<decltype(q)::value>(w[i], x[j], c, sa[i], sb[j]);
+        // here and nowhere else: the compiler takes this instruction for one that it
+        // may sink, and would gather all products behind the stage's last branch
+        asm volatile("" : "+a"(acc[i][j]));
     };
-    auto read_step = [&](int r, int buf, int ks0, v4i (&w)[KSL][C::FN], v4i (&x)[KSL][C::FM]) {
-        if (r >= KSL * NDS) return;
-        const int ks = r / NDS, rr = r % NDS;
-        if (rr < C::FN) w[ks][rr] = frag_a(buf, rr, ks0 + ks);
-        else x[ks][rr - C::FN] = frag_b(buf, rr - C::FN, ks0 + ks);
+    auto read_step = [&](int r, int off, v4i (&w)[C::FN], v4i (&x)[C::FM]) {
+        if (r < C::FN) w[r] = frag_a(off, r);
+        else if (r < NDS) x[r - C::FN] = frag_b(off, r - C::FN);
     };
-    auto read_scale = [&](int r, int d) {
-        if (r < C::FN) na[r] = scale(d, (wn0 >> 5) + r);
-        else if (r < NDS) nb[r - C::FN] = scale(d, BN / 32 + (wm0 >> 5) + r - C::FN);
+    auto read_scale = [&](int r, uint32_t slot) {
+        if (r < C::FN) na[r] = scale(slot, (wn0 >> 5) + r);
+        else if (r < NDS) nb[r - C::FN] = scale(slot, BN / 32 + (wm0 >> 5) + r - C::FN);
     };
-
-    constexpr int STEPS = KSL * (NMF > NDS ? NMF : NDS);
-    constexpr int STEPS0 = !SPREAD && C::L > STEPS ? C::L : STEPS;
-    constexpr int STEPS1 = STEPS > NDS ? STEPS : NDS;
-    // Stage s, of parity PAR in its unit (KSL 1: which half of the scales' k).
-    auto stage = [&](int s, int kt, auto first, auto par, bool after_epilogue) {
+    constexpr int STEPS = NMF > NDS ? NMF : NDS;
+    // loads [P0, P1) of the stage ahead, spread over the steps of a half (a burst of
+    // them fills the address unit's queue and holds up the products behind it)
+    auto spread = [&](int k, auto p0, auto p1, uint32_t at) {
+        constexpr int P0 = decltype(p0)::value, P1 = decltype(p1)::value;
+        if constexpr (P1 > P0) {
+            constexpr int EVERY = STEPS / (P1 - P0);
+            for_each<P1 - P0>([&](auto i) {
+                if (k == i * EVERY + EVERY / 2) issue(std::integral_constant<int, P0 + decltype(i)::value>{}, at);
+            });
+        }
+    };
+    // One stage, of parity PAR in its pair.  It loads the stage 3 ahead into the slot
+    // of the one before it: of the pair's own first slot when odd, of the other
+    // side's second when even.  STORES: the stores of an epilogue may still be
+    // counted.
+    auto stage = [&](auto first, auto par, bool stores) {
         constexpr int PAR = decltype(par)::value;
-        constexpr bool LOADS_SCALES = KSL == 2 || PAR == 1;   // the stage P = 3 ahead begins a chunk
-        constexpr bool READS_SCALES = KSL == 2 || PAR == 1;   // so does the next one
-        const int buf = (int)((unsigned)s % C::NBUF), nbuf = (int)((unsigned)(s + 1) % C::NBUF);
-        const uint32_t lslot = smem_addr + (uint32_t)(((unsigned)(s + C::P) % C::NBUF) * C::CODES);
+        const uint32_t at = ring + (PAR ? cur : cur ^ 1u) * (2 * C::CODES) + (PAR ? 0 : C::CODES);
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (LOADS_SCALES) issue_scales(KSL == 2 ? s + C::P : (s + C::P) / 2);
+        if constexpr (PAR == 1) issue_scales(cur);
 #pragma unroll
-        for (int k = 0; k < STEPS0; ++k) {
-            if (k < KSL * NMF) mfma_step(k, std::integral_constant<int, KSL == 2 ? 0 : 2 * PAR>{}, fa, fb, decltype(first)::value);
-            read_step(k, buf, KSL, ga, gb);
-            if constexpr (SPREAD) {
-                constexpr int SP = STEPS / HL;
-                if (k % SP == SP / 2 && k / SP < HL) issue_one(k / SP, lslot);
-            } else {
-                if (k < C::L) issue_one(k, lslot);
-            }
+        for (int k = 0; k < STEPS; ++k) {
+            if (k < NMF) mfma_step(k, std::integral_constant<int, 2 * PAR>{}, fa, fb, decltype(first)::value);
+            read_step(k, PAR * C::CODES + 1024, ga, gb);
+            spread(k, std::integral_constant<int, 0>{}, std::integral_constant<int, H0>{}, at);
             __builtin_amdgcn_sched_barrier(0);
         }
-        if constexpr (!SPREAD) advance();
-
         wait_lgkmcnt0();              // this wave's fragments of the second half are in registers
-        if (kt <= C::P - 2 && after_epilogue) wait_vmcnt<OUTS + NST>();
+        if (stores) wait_vmcnt<OUTS + NST>();
         else wait_vmcnt<OUTS>();
-        workgroup_barrier();          // every wave's; stage s + 1 is in LDS, and slot s is read no more
+        workgroup_barrier();          // every wave's; the next stage is in LDS, and this one's slot is read no more
+        if constexpr (PAR == 1) pa += side, pb += side;
 #pragma unroll
-        for (int k = 0; k < STEPS1; ++k) {
-            if (k < KSL * NMF) mfma_step(k, std::integral_constant<int, KSL == 2 ? 2 : 2 * PAR + 1>{}, ga, gb, false);
-            read_step(k, nbuf, 0, fa, fb);
-            if constexpr (READS_SCALES) read_scale(k, KSL == 2 ? s + 1 : (s + 1) / 2);
-            if constexpr (SPREAD) {
-                constexpr int SP = STEPS / (C::L - HL);
-                if (k % SP == SP / 2 && k / SP < C::L - HL) issue_one(HL + k / SP, lslot);
-            }
+        for (int k = 0; k < STEPS; ++k) {
+            if (k < NMF) mfma_step(k, std::integral_constant<int, 2 * PAR + 1>{}, ga, gb, false);
+            read_step(k, PAR ? 0 : C::CODES, fa, fb);
+            if constexpr (PAR == 1) read_scale(k, cur ^ 1u);
+            spread(k, std::integral_constant<int, H0>{}, std::integral_constant<int, NPAIR>{}, at);
             __builtin_amdgcn_sched_barrier(0);
         }
-        if constexpr (SPREAD) advance();
-        if constexpr (READS_SCALES) {
+        next_stage();
+        if constexpr (PAR == 0) next_pair();
+        else {
+            side = -side;
+            cur ^= 1u;
 #pragma unroll
             for (int i = 0; i < C::FN; ++i) sa[i] = na[i];
 #pragma unroll
@@ -338,8 +377,8 @@ __global__ __launch_bounds__(256) void mx4_gemm_kernel(Args g)
     // registers 4 qd .. 4 qd + 3, rows 8 qd + 4 (l / 32) + 0..3 (four consecutive
     // n).  Lanes l and l + 32 exchange halves so that each has 8 consecutive n.
     // Rows past M lie outside the buffer of the tile's rows, columns past N are
-    // given an offset outside it: both stores are dropped.
-    auto epilogue = [&](int u) {
+    // given an offset outside it: both stores are dropped.  Fragments j0 <= j < j1.
+    auto epilogue = [&](int u, int j0, int j1) {
         int tm, tn;
         tile_coords(u % tiles, g.tiles_m, g.tiles_n, g.group_m, tm, tn);
         const int64_t row0 = (int64_t)tm * BM;
@@ -350,6 +389,7 @@ __global__ __launch_bounds__(256) void mx4_gemm_kernel(Args g)
         const int n_base = tn * BN + wn0 + 8 * lh;
 #pragma unroll
         for (int j = 0; j < C::FM; ++j) {
+            if (j < j0 || j >= j1) continue;
             const int r = wm0 + 32 * j + lr;
             const uint32_t row = (uint32_t)r * (uint32_t)g.N;
 #pragma unroll
@@ -410,24 +450,74 @@ __global__ __launch_bounds__(256) void mx4_gemm_kernel(Args g)
         }
     };
 
-    int s = 0;
     constexpr std::integral_constant<int, 0> even{};
     constexpr std::integral_constant<int, 1> odd{};
-    for (int q = 0; q < my_units; ++q) {
-        if constexpr (KSL == 1) {   // KT is even: a padded row holds whole chunks of scales
-            stage(s++, 0, std::true_type{}, even, q > 0);
-            stage(s++, 1, std::false_type{}, odd, q > 0);
-            for (int kt = 2; kt < KT; kt += 2) {
-                stage(s++, kt, std::false_type{}, even, q > 0);
-                stage(s++, kt + 1, std::false_type{}, odd, q > 0);
+    if constexpr (GROUPS == 1) {
+        for (int q = 0; q < my_units; ++q) {
+            stage(std::true_type{}, even, q > 0);
+            stage(std::false_type{}, odd, q > 0);
+            for (int p = 1; p < pairs; ++p) {
+                stage(std::false_type{}, even, false);
+                stage(std::false_type{}, odd, false);
             }
-        } else {
-            stage(s++, 0, std::true_type{}, even, q > 0);
-            for (int kt = 1; kt < KT; ++kt) stage(s++, kt, std::false_type{}, even, q > 0);
+            epilogue(unit_of(q), 0, C::FM);
         }
-        epilogue(unit_of(q));
+        wait_vmcnt<0>();   // no LDS load may land after the workgroup retires
+    } else {
+        stage(std::true_type{}, even, false);
+        stage(std::false_type{}, odd, false);
+        for (int p = 1; p < pairs; ++p) {
+            stage(std::false_type{}, even, false);
+            stage(std::false_type{}, odd, false);
+        }
+        if (pairs < most_pairs) {   // as many barriers in every group
+            workgroup_barrier();
+            workgroup_barrier();
+        }
+        // The groups' sums: group o keeps fragments j of its share (all of them in
+        // group 0 where there are fewer than groups), the others give theirs in LDS.
+        wait_vmcnt<0>();
+        wait_lgkmcnt0();
+        workgroup_barrier();        // the rings are read no more and nothing lands in them
+        constexpr int OWNERS = C::FM >= GROUPS ? GROUPS : 1, SHARE = C::FM / OWNERS;
+        static_assert(C::FM % OWNERS == 0, "shares");
+        static_assert(4 * OWNERS * (GROUPS - 1) * C::FN * SHARE * 4096 <= C::LDS, "LDS of the sums");
+        // [owner][giver, but the owner][wave][i][j of the share][4 registers][lane]
+        auto place = [&](int owner, int giver, int i, int j) {
+            const int slot = giver < owner ? giver : giver - 1;
+            return smem + ((((owner * (GROUPS - 1) + slot) * 4 + wave) * C::FN + i) * SHARE + j) * 4096 + lane * 16;
+        };
+#pragma unroll
+        for (int j = 0; j < C::FM; ++j) {
+            const int owner = j / SHARE;
+            if (owner == group) continue;
+#pragma unroll
+            for (int i = 0; i < C::FN; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<v4f*>(place(owner, group, i, j % SHARE) + q * 1024) =
+                        v4f{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        }
+        __syncthreads();
+        if (group >= OWNERS) return;
+#pragma unroll
+        for (int j = 0; j < C::FM; ++j) {
+            if (j / SHARE != group) continue;
+#pragma unroll
+            for (int o = 0; o < GROUPS; ++o) {
+                if (o == group) continue;
+#pragma unroll
+                for (int i = 0; i < C::FN; ++i)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const v4f t = *reinterpret_cast<const v4f*>(place(group, o, i, j % SHARE) + q * 1024);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += t[e];
+                    }
+            }
+        }
+        epilogue(unit_of(0), group * SHARE, (group + 1) * SHARE);
     }
-    wait_vmcnt<0>();   // no LDS load may land after the workgroup retires
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
@@ -458,40 +548,38 @@ __global__ __launch_bounds__(256) void mx4_join_kernel(const float* __restrict__
     *reinterpret_cast<uint4*>(y + at) = pack8<bf16>(v);
 }
 
-template <int BM, int BN, int KSL>
+template <int BM, int BN, int GROUPS>
 hipError_t launch(Args g, int num_cu, hipStream_t st)
 {
-    using C = Cfg<BM, BN, KSL>;
     const bool part = g.splits > 1, extra = g.ex.bias || g.ex.res;
     g.tiles_m = (g.M + BM - 1) / BM;
     g.tiles_n = (g.N + BN - 1) / BN;
     g.group_m = std::min(g.tiles_m, 4);
-    g.stages = g.kb / C::KS2 / g.splits;
     const int units = g.tiles_m * g.tiles_n * g.splits;
-    const int slots = num_cu * (160 * 1024 / C::LDS);
-    const dim3 grid(std::min(units, slots)), block(256);
+    const dim3 grid(GROUPS > 1 ? units : std::min(units, num_cu)), block(256 * GROUPS);
     if (part)
-        mx4_gemm_kernel<BM, BN, KSL, true, false><<<grid, block, 0, st>>>(g);
+        mx4_gemm_kernel<BM, BN, GROUPS, true, false><<<grid, block, 0, st>>>(g);
     else if (extra)
-        mx4_gemm_kernel<BM, BN, KSL, false, true><<<grid, block, 0, st>>>(g);
+        mx4_gemm_kernel<BM, BN, GROUPS, false, true><<<grid, block, 0, st>>>(g);
     else
-        mx4_gemm_kernel<BM, BN, KSL, false, false><<<grid, block, 0, st>>>(g);
+        mx4_gemm_kernel<BM, BN, GROUPS, false, false><<<grid, block, 0, st>>>(g);
     return hipGetLastError();
 }
 
-// How a product runs: which tiles, over how many splits of k.
+// How a product runs: which tiles, how many groups a workgroup, over how many splits of k.
 struct Plan {
-    int bm, bn, splits;
+    int bm, bn, groups, splits;
 };
 
 Plan plan_of(int64_t m, int64_t n, int64_t k, int num_cu)
 {
     auto tiles = [&](int bm, int bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); };
-    const int64_t units = pad_cols(k) / 256;
-    if (tiles(256, 256) >= num_cu) return {256, 256, 1};
-    if (tiles(128, 128) >= num_cu / 2) return {128, 128, 1};
-    Plan p{64, 64, 1};
-    while (tiles(64, 64) * p.splits * 2 <= num_cu && units % (p.splits * 2) == 0 && units / (p.splits * 2) >= 4) p.splits *= 2;
+    const int64_t pairs = pad_cols(k) / 256;
+    if (pairs == 1 || tiles(256, 256) >= num_cu) return {256, 256, 1, 1};
+    if (tiles(128, 128) >= num_cu / 2) return {128, 128, 2, 1};
+    Plan p{64, 64, 2, 1};
+    if (pairs >= 4) p.groups = 4;
+    while (tiles(64, 64) * p.splits * 2 <= num_cu && pairs / (p.splits * 2) >= 4) p.splits *= 2;
     return p;
 }
 
@@ -515,9 +603,10 @@ hipError_t launch_mx4_gemm(const uint8_t* xc, const uint8_t* xs, const uint8_t* 
     g.splits = p.splits;
     g.out = p.splits > 1 ? workspace : y;
     if (p.splits == 1) g.ex = ex;
-    hipError_t e = p.bm == 256   ? mx4::launch<256, 256, 1>(g, num_cu, st)
-                   : p.bm == 128 ? mx4::launch<128, 128, 2>(g, num_cu, st)
-                                 : mx4::launch<64, 64, 2>(g, num_cu, st);
+    hipError_t e = p.bm == 256     ? mx4::launch<256, 256, 1>(g, num_cu, st)
+                   : p.bm == 128   ? mx4::launch<128, 128, 2>(g, num_cu, st)
+                   : p.groups == 4 ? mx4::launch<64, 64, 4>(g, num_cu, st)
+                                   : mx4::launch<64, 64, 2>(g, num_cu, st);
     if (e != hipSuccess || p.splits == 1) return e;
     const int64_t threads = m * n / 8;
     mx4::mx4_join_kernel<<<dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, st>>>(
