@@ -140,6 +140,11 @@ struct Cfg {
     static constexpr int CPW = (CHUNKS + 3) / 4;        // chunks a wave loads, into its own KB
     static constexpr int RING = 4 * CODES + 2 * 4096;   // 4 slots of codes, 2 of scales
     static constexpr int LDS = GROUPS * RING;
+    // the groups' sums: group o keeps fragments j of its share (all of them in group
+    // 0 where there are fewer than groups), the others give theirs in LDS
+    static constexpr int OWNERS = FM >= GROUPS ? GROUPS : 1, SHARE = FM / OWNERS;
+    static constexpr int SUMS = 4 * OWNERS * (GROUPS - 1) * FN * SHARE * 4096;
+    static_assert(FM % OWNERS == 0, "shares");
     static_assert(LDS <= 160 * 1024, "LDS");
     static_assert(A_BLK % 4 == 0 && B_BLK % 4 == 0, "blocks split evenly over 4 waves");
 };
@@ -173,7 +178,10 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
     // The body uses AMDGPU-only types; the host pass only needs the launch stub.
 #if defined(__HIP_DEVICE_COMPILE__)
     using C = Cfg<BM, BN, GROUPS>;
-    __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
+    // the rings; then the tile's bias, or (GROUPS > 1) the groups' sums and the bias in place of the rings
+    constexpr int SUMS = GROUPS > 1 ? C::SUMS : C::LDS;
+    static_assert(GROUPS == 1 || SUMS + BN * 4 <= C::LDS, "LDS of the sums");
+    __shared__ __attribute__((aligned(1024))) char smem[C::LDS + (GROUPS == 1 && EXTRA ? BN * 4 : 0)];
     constexpr int NMF = C::FN * C::FM;                  // products of a slice
     constexpr int NDS = C::FN + C::FM;                  // fragment reads of a slice
     constexpr int NPAIR = C::AP + C::XP;                // loads (of one or two KB) of a stage
@@ -305,7 +313,9 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
 
     // Product k of a slice, slice Q of the pair.
     auto mfma_step = [&](int k, auto q, const v4i (&w)[C::FN], const v4i (&x)[C::FM], bool zero) {
-        const int i = k / C::FM, j = k % C::FM;
+        // back and forth over j, so that consecutive products share an operand (the
+        // operands' switching is power, and power is speed: 0.5% on large products)
+        const int i = k / C::FM, j = i % 2 ? C::FM - 1 - k % C::FM : k % C::FM;
         const v16f c = zero ? v16f{} : acc[i][j];
         acc[i][j] = product<decltype(q)::value>(w[i], x[j], c, sa[i], sb[j]);
         // here and nowhere else: the compiler takes this instruction for one that it
@@ -378,6 +388,10 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
     // n).  Lanes l and l + 32 exchange halves so that each has 8 consecutive n.
     // Rows past M lie outside the buffer of the tile's rows, columns past N are
     // given an offset outside it: both stores are dropped.  Fragments j0 <= j < j1.
+    auto stage_bias = [&](int tn) {
+        const int t = (int)threadIdx.x;
+        if (t < BN) reinterpret_cast<float*>(smem + SUMS)[t] = g.ex.bias[min(tn * BN + t, g.N - 1)];
+    };
     auto epilogue = [&](int u, int j0, int j1) {
         int tm, tn;
         tile_coords(u % tiles, g.tiles_m, g.tiles_n, g.group_m, tm, tn);
@@ -387,11 +401,33 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
         char* base = static_cast<char*>(g.out) + ((PART ? (int64_t)(u / tiles) * g.M : 0) + row0) * g.N * B;
         const __amdgpu_buffer_rsrc_t rs_o = __builtin_amdgcn_make_buffer_rsrc(base, (short)0, rows * g.N * B, 0x00020000);
         const int n_base = tn * BN + wn0 + 8 * lh;
+        // The residual's row j is loaded while row j - 1 is stored; the bias, which
+        // every row needs, waits in LDS.
+        constexpr int PER_ROW = EXTRA ? C::FN * 2 : 1;
+        uint4 res[2][PER_ROW];
+        auto load_residual = [&](int j) {
+            const int64_t row = (row0 + min(wm0 + 32 * j + lr, rows - 1)) * g.N;
+#pragma unroll
+            for (int t = 0; t < PER_ROW; ++t)
+                res[j & 1][t] = *reinterpret_cast<const uint4*>(g.ex.res + row + min(n_base + 16 * t, g.N - 8));
+        };
+        if constexpr (EXTRA) {
+            if (g.ex.res) load_residual(j0);
+            if (GROUPS == 1 && g.ex.bias) {   // the last tile's readers have passed the stages' barriers
+                stage_bias(tn);
+                wait_lgkmcnt0();
+                workgroup_barrier();
+            }
+        }
 #pragma unroll
         for (int j = 0; j < C::FM; ++j) {
             if (j < j0 || j >= j1) continue;
             const int r = wm0 + 32 * j + lr;
             const uint32_t row = (uint32_t)r * (uint32_t)g.N;
+            if constexpr (EXTRA) {
+                if (g.ex.res && j + 1 < j1) load_residual(j + 1);
+                __builtin_amdgcn_sched_barrier(0);
+            }
 #pragma unroll
             for (int i = 0; i < C::FN; ++i) {
                 // one fragment out of the accumulators here, not all of them up front
@@ -425,20 +461,16 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
                             __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, v4f{v[4], v[5], v[6], v[7]}), rs_o,
                                                                    r < rows && ok ? o + 16u : kBufferOutside, 0, 0);
                         } else {
-                            const int nn = min(n, g.N - 8);
                             if (g.ex.bias) {
-                                float bias[8];
-                                *reinterpret_cast<float4*>(bias) = *reinterpret_cast<const float4*>(g.ex.bias + nn);
-                                *reinterpret_cast<float4*>(bias + 4) = *reinterpret_cast<const float4*>(g.ex.bias + nn + 4);
+                                const float* lb = reinterpret_cast<const float*>(smem + SUMS) + wn0 + 8 * lh + 32 * i + 16 * h;
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) v[e] = v[e] + bias[e];
+                                for (int e = 0; e < 8; ++e) v[e] = v[e] + lb[e];
                             }
                             if (g.ex.res) {
-                                float res[8];
-                                unpack8<bf16>(*reinterpret_cast<const uint4*>(
-                                                  g.ex.res + (row0 + min(r, rows - 1)) * g.N + nn), res);
+                                float x[8];
+                                unpack8<bf16>(res[j & 1][2 * i + h], x);
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) v[e] = v[e] + res[e];
+                                for (int e = 0; e < 8; ++e) v[e] = v[e] + x[e];
                             }
                             __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, pack8<bf16>(v)), rs_o,
                                                                    ok ? (row + (uint32_t)n) * 2u : kBufferOutside, 0, 0);
@@ -474,14 +506,10 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
             workgroup_barrier();
             workgroup_barrier();
         }
-        // The groups' sums: group o keeps fragments j of its share (all of them in
-        // group 0 where there are fewer than groups), the others give theirs in LDS.
         wait_vmcnt<0>();
         wait_lgkmcnt0();
         workgroup_barrier();        // the rings are read no more and nothing lands in them
-        constexpr int OWNERS = C::FM >= GROUPS ? GROUPS : 1, SHARE = C::FM / OWNERS;
-        static_assert(C::FM % OWNERS == 0, "shares");
-        static_assert(4 * OWNERS * (GROUPS - 1) * C::FN * SHARE * 4096 <= C::LDS, "LDS of the sums");
+        constexpr int OWNERS = C::OWNERS, SHARE = C::SHARE;
         // [owner][giver, but the owner][wave][i][j of the share][4 registers][lane]
         auto place = [&](int owner, int giver, int i, int j) {
             const int slot = giver < owner ? giver : giver - 1;
@@ -497,6 +525,11 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
                 for (int q = 0; q < 4; ++q)
                     *reinterpret_cast<v4f*>(place(owner, group, i, j % SHARE) + q * 1024) =
                         v4f{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        }
+        if (EXTRA && g.ex.bias) {
+            int tm, tn;
+            tile_coords(unit_of(0) % tiles, g.tiles_m, g.tiles_n, g.group_m, tm, tn);
+            stage_bias(tn);
         }
         __syncthreads();
         if (group >= OWNERS) return;
