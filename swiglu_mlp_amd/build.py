@@ -22,7 +22,7 @@ LIB = os.path.join(HERE, "libck_convrot.so")
 MARSHAL = os.path.join(HERE, "_marshal.so")
 SOURCES = ["api.hip", "quant.hip", "gemm.hip", "gemm_big.hip", "gemm_blk.hip", "gemm_small.hip",
            "gemm_fused.hip", "qknorm.hip", "attn.hip", "attn_bf16.hip",
-           "attn_fp16.hip", "api_block.hip", "mx4_quant.hip", "mx4_gemm.hip",
+           "attn_fp16.hip", "api_block.hip", "mx4_quant.hip", "mx4_gemm.hip", "mx4_few.hip",
            "block_norm.hip", "probe.hip"]
 ARCH = "gfx950"
 

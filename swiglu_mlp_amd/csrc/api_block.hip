@@ -146,6 +146,9 @@ ck_status ck_mx4_linear(const uint16_t* x, int64_t ldx, int32_t act, const uint8
     CK_TRY(check_epilogue(bias, residual, y));
     if (!good_workspace(workspace, workspace_bytes, ck_mx4_linear_workspace_size(m, k, n))) return CK_EWORKSPACE;
     hipStream_t st = (hipStream_t)stream;
+    if (ck::mx4_fused(m, k))   // the quantizer inside the product: one launch, the workspace untouched
+        return from_hip(ck::launch_mx4_fused(act == CK_ACT_SWIGLU ? 1 : 0, x, ldx, w_codes, w_scales, m, n, k, group, y,
+                                             ck::EpiExtra{bias, residual}, st));
     uint8_t* xc = static_cast<uint8_t*>(workspace);
     uint8_t* xs = xc + round_up(codes_bytes(m, k));
     CK_TRY(from_hip(ck::launch_mx4_quant(act == CK_ACT_SWIGLU ? 1 : 0, x, ldx, m, k, group, true, xc, xs, st)));

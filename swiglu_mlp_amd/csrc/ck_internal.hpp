@@ -165,6 +165,15 @@ size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k);
 hipError_t launch_mx4_gemm(const uint8_t* xc, const uint8_t* xs, const uint8_t* wc, const uint8_t* ws, int64_t m,
                            int64_t n, int64_t k, uint16_t* y, EpiExtra ex, void* workspace, hipStream_t st);
 
+// The same for few rows (mx4_few.hip), and with the quantizer in the same kernel
+// for the fewest (x BF16 [m, ldx], act as in launch_mx4_quant).
+bool mx4_few_rows(int64_t m, int64_t n, int64_t k);
+hipError_t launch_mx4_few(const uint8_t* xc, const uint8_t* xs, const uint8_t* wc, const uint8_t* ws, int64_t m, int64_t n,
+                          int64_t k, uint16_t* y, EpiExtra ex, hipStream_t st);
+bool mx4_fused(int64_t m, int64_t k);
+hipError_t launch_mx4_fused(int act, const uint16_t* x, int64_t ldx, const uint8_t* wc, const uint8_t* ws, int64_t m,
+                            int64_t n, int64_t k, int g, uint16_t* y, EpiExtra ex, hipStream_t st);
+
 // Residual sum with the branch's norm and gate, and the next norm with its
 // modulation (block_norm.hip).  Strides in elements; null pointers: absent.
 struct ModArgs {

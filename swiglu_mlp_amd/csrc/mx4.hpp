@@ -122,5 +122,39 @@ __device__ __forceinline__ uint4 quantize32(float (&v)[4][8], int lane, uint32_t
     return make_uint4(codes8(v[0], s) ^ flip, codes8(v[1], s) ^ flip, codes8(v[2], s) ^ flip, codes8(v[3], s) ^ flip);
 }
 
+// 32 values from element `at` on.  KIND 0: BF16 x; 1: BF16 [gate | up] (up k
+// further), silu(gate) * up; 2: FP32.
+template <int KIND>
+__device__ __forceinline__ void load32(const void* __restrict__ src, int64_t at, int64_t k, float (&v)[4][8])
+{
+    if constexpr (KIND == 2) {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(src) + at);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            *reinterpret_cast<float4*>(v[j]) = p[2 * j];
+            *reinterpret_cast<float4*>(v[j] + 4) = p[2 * j + 1];
+        }
+    } else {
+        const uint16_t* x = static_cast<const uint16_t*>(src) + at;
+        uint4 a[4], b[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[j] = reinterpret_cast<const uint4*>(x)[j];
+        if constexpr (KIND == 1) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) b[j] = reinterpret_cast<const uint4*>(x + k)[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            unpack8<bf16>(a[j], v[j]);
+            if constexpr (KIND == 1) {
+                float u[8];
+                unpack8<bf16>(b[j], u);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[j][i] = silu_mul(v[j][i], u[i]);
+            }
+        }
+    }
+}
+
 }  // namespace mx4
 }  // namespace ck

@@ -620,6 +620,7 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, int num_cu)
 
 size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k)
 {
+    if (mx4_few_rows(m, n, k)) return 0;
     const mx4::Plan p = mx4::plan_of(m, n, k, num_cus());
     return p.splits > 1 ? (size_t)p.splits * (size_t)m * (size_t)n * 4 : 0;
 }
@@ -627,6 +628,7 @@ size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k)
 hipError_t launch_mx4_gemm(const uint8_t* xc, const uint8_t* xs, const uint8_t* wc, const uint8_t* ws, int64_t m,
                            int64_t n, int64_t k, uint16_t* y, EpiExtra ex, void* workspace, hipStream_t st)
 {
+    if (mx4_few_rows(m, n, k)) return launch_mx4_few(xc, xs, wc, ws, m, n, k, y, ex, st);
     const int num_cu = num_cus();
     const mx4::Plan p = mx4::plan_of(m, n, k, num_cu);
     mx4::Args g{};

@@ -14,39 +14,6 @@
 namespace ck {
 namespace mx4 {
 
-// KIND 0: BF16 x; 1: BF16 [gate | up], silu(gate) * up; 2: FP32.
-template <int KIND>
-__device__ __forceinline__ void load32(const void* __restrict__ src, int64_t at, int64_t k, float (&v)[4][8])
-{
-    if constexpr (KIND == 2) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(src) + at);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            *reinterpret_cast<float4*>(v[j]) = p[2 * j];
-            *reinterpret_cast<float4*>(v[j] + 4) = p[2 * j + 1];
-        }
-    } else {
-        const uint16_t* x = static_cast<const uint16_t*>(src) + at;
-        uint4 a[4], b[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) a[j] = reinterpret_cast<const uint4*>(x)[j];
-        if constexpr (KIND == 1) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) b[j] = reinterpret_cast<const uint4*>(x + k)[j];
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            unpack8<bf16>(a[j], v[j]);
-            if constexpr (KIND == 1) {
-                float u[8];
-                unpack8<bf16>(b[j], u);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[j][i] = silu_mul(v[j][i], u[i]);
-            }
-        }
-    }
-}
-
 template <int KIND, int LOG_G, bool BLOCKED>
 __global__ __launch_bounds__(256) void mx4_quant_kernel(const void* __restrict__ src, int64_t ld, int64_t m, int64_t k,
                                                         uint32_t units, uint8_t* __restrict__ codes,
