@@ -65,11 +65,12 @@ __device__ __forceinline__ uint4 quantize32_by(int log_g, float (&v)[4][8], int 
 }
 
 // NA x MF fragments of 16 x 16 a workgroup.  ACT (FUSED): 0 x, 1 silu(gate) * up.
+// Two workgroups a CU (at most 128 registers), but for 128 rows of x.
 template <int NA, int MF, bool FUSED, int ACT>
-__global__ __launch_bounds__(kThreads) void mx4_few_kernel(FewArgs g)
+__global__ __launch_bounds__(kThreads, MF > 4 ? 2 : 4) void mx4_few_kernel(FewArgs g)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
-    constexpr int UB = NA + MF <= 2 ? 4 : NA + MF <= 3 ? 3 : NA + MF <= 6 ? 2 : 1;   // pairs of a batch
+    constexpr int UB = (FUSED ? NA : NA + MF) <= 3 ? 2 : 1;   // pairs of a batch
     constexpr int F = NA * MF;
     constexpr int CODES = FUSED ? kFusedValues / 2 : 0, SCALES = FUSED ? kFusedValues / 32 : 0;
     constexpr int RED = kWaves * F * 1024;
@@ -237,17 +238,13 @@ hipError_t launch_few(const FewArgs& g, hipStream_t st)
     return hipGetLastError();
 }
 
-template <int MF>
-hipError_t pick_few(const FewArgs& g, int num_cu, hipStream_t st)
-{
-    if (g.N >= 64 * num_cu && MF <= 4) return launch_few<MF <= 4 ? 4 : 1, MF, false, 0>(g, st);
-    if (g.N >= 32 * num_cu) return launch_few<2, MF, false, 0>(g, st);
-    return launch_few<1, MF, false, 0>(g, st);
-}
-
 }  // namespace mx4
 
-bool mx4_few_rows(int64_t m, int64_t, int64_t) { return m <= 64; }
+bool mx4_few_rows(int64_t m, int64_t n, int64_t)
+{
+    const int64_t cus = num_cus();
+    return m <= 32 || (m <= 64 && n < 32 * cus) || (m <= 128 && n <= 16 * cus);
+}
 
 hipError_t launch_mx4_few(const uint8_t* xc, const uint8_t* xs, const uint8_t* wc, const uint8_t* ws, int64_t m, int64_t n,
                           int64_t k, uint16_t* y, EpiExtra ex, hipStream_t st)
@@ -256,10 +253,11 @@ hipError_t launch_mx4_few(const uint8_t* xc, const uint8_t* xs, const uint8_t* w
     g.xc = xc, g.xs = xs, g.wc = wc, g.ws = ws, g.y = y, g.ex = ex;
     g.M = (int)m, g.N = (int)n, g.k = (int)k, g.pairs = (int)(mx4::pad_cols(k) / 256);
     g.xb = (int)(mx4::pad_rows(m) / 32), g.wb = (int)(mx4::pad_rows(n) / 32);
-    const int num_cu = num_cus();
-    if (m <= 16) return mx4::pick_few<1>(g, num_cu, st);
-    if (m <= 32) return mx4::pick_few<2>(g, num_cu, st);
-    return mx4::pick_few<4>(g, num_cu, st);
+    const bool wide = n >= 32 * num_cus();   // 32 rows of the weight a workgroup still give every CU one
+    if (m <= 16) return wide ? mx4::launch_few<2, 1, false, 0>(g, st) : mx4::launch_few<1, 1, false, 0>(g, st);
+    if (m <= 32) return wide ? mx4::launch_few<2, 2, false, 0>(g, st) : mx4::launch_few<1, 2, false, 0>(g, st);
+    if (m <= 64) return mx4::launch_few<1, 4, false, 0>(g, st);
+    return mx4::launch_few<1, 8, false, 0>(g, st);
 }
 
 bool mx4_fused(int64_t m, int64_t k)

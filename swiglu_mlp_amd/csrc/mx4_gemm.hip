@@ -17,8 +17,8 @@
 //  * A group of 4 waves (2 x 2) owns a BM x BN tile; a wave's part is FM x FN
 //    fragments of 32 x 32, accumulated in AGPRs.  It reads FM + FN blocks from
 //    LDS for FM FN products.
-//  * K advances two slices (128 values) a stage.  Stages go through a ring of 4
-//    LDS slots by DMA (buffer_load ... lds, two for one LDS address), 3 ahead.  A
+//  * K advances two slices (128 values) a stage.  Stages go through a ring of LDS
+//    slots by DMA (buffer_load ... lds, two for one LDS address), 3 or more ahead.  A
 //    stage is two halves around one barrier: each multiplies one slice while it
 //    reads the next one's fragments, so products never wait for LDS.  Reads and
 //    loads are placed between the products in source order.
@@ -131,6 +131,9 @@ __device__ __forceinline__ void for_each(F&& f)
 template <int BM_, int BN_, int GROUPS_>
 struct Cfg {
     static constexpr int BM = BM_, BN = BN_, GROUPS = GROUPS_;
+    // Pairs of stages in the ring, and stages ahead.  3 and 4 pairs, where they fit,
+    // were no faster (64 x 64 tiles: 7.7 to 7.9 us for 256 x 4096 -> 4096).
+    static constexpr int R = 2, P = 2 * R - 1;
     static constexpr int FM = BM / 64, FN = BN / 64;    // a wave's fragments
     static constexpr int A_BLK = BN / 16, B_BLK = BM / 16;              // 1 KB blocks of a stage
     static constexpr int AW = A_BLK / 4, XW = B_BLK / 4, L = AW + XW;   // a wave's share
@@ -138,7 +141,7 @@ struct Cfg {
     static constexpr int CODES = (A_BLK + B_BLK) * 1024;
     static constexpr int CHUNKS = (BM + BN) / 32;       // of scales (32 rows, 256 k)
     static constexpr int CPW = (CHUNKS + 3) / 4;        // chunks a wave loads, into its own KB
-    static constexpr int RING = 4 * CODES + 2 * 4096;   // 4 slots of codes, 2 of scales
+    static constexpr int RING = R * (2 * CODES + 4096); // slots of codes, then of scales
     static constexpr int LDS = GROUPS * RING;
     // the groups' sums: group o keeps fragments j of its share (all of them in group
     // 0 where there are fewer than groups), the others give theirs in LDS
@@ -171,13 +174,14 @@ __device__ __forceinline__ void tile_coords(int j, int tiles_m, int tiles_n, int
     tn = (j % width) / gm;
 }
 
-// PART: FP32 partial sums out.  EXTRA: bias and / or residual.
+// PART: FP32 partial sums out (64 x 64 tiles).  EXTRA: bias and / or residual.
 template <int BM, int BN, int GROUPS, bool PART, bool EXTRA>
 __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
 {
     // The body uses AMDGPU-only types; the host pass only needs the launch stub.
 #if defined(__HIP_DEVICE_COMPILE__)
     using C = Cfg<BM, BN, GROUPS>;
+    constexpr int R = C::R;
     // the rings; then the tile's bias, or (GROUPS > 1) the groups' sums and the bias in place of the rings
     constexpr int SUMS = GROUPS > 1 ? C::SUMS : C::LDS;
     static_assert(GROUPS == 1 || SUMS + BN * 4 <= C::LDS, "LDS of the sums");
@@ -190,8 +194,8 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
                        (H0 > C::AP ? H0 - C::AP : 0) * (C::XW > 1 ? 2 : 1);   // as instructions
     constexpr int NST = PART ? 0 : 2 * NMF;             // stores of an epilogue (PART: too many to count, waited for)
     // Loads issued after the last of stage s + 1 at the middle of stage s: those of
-    // s + 2, the first half's of s + 3, and the scales with one of the two.
-    constexpr int OUTS = C::L + L0 + 1;
+    // s + 2 .. s + P - 1, the first half's of s + P, and the scales with every second one of these.
+    constexpr int OUTS = (C::P - 2) * C::L + L0 + R - 1;
     static_assert(OUTS + NST < 64, "vmcnt range");
 
     const int lane = threadIdx.x & 63;
@@ -261,7 +265,7 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
                                                                      at + (uint32_t)(wave * C::XW * 1024));
     };
     auto issue_scales = [&](uint32_t slot) {
-        lds_dma(sp, ring + 4 * C::CODES + slot * 4096 + (uint32_t)wave * 1024);
+        lds_dma(sp, ring + 2 * R * C::CODES + slot * 4096 + (uint32_t)wave * 1024);
         sp += 256;
     };
     auto next_stage = [&]() {
@@ -282,12 +286,11 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
     v16f acc[C::FN][C::FM];
     const int lr = lane & 31, lh = lane >> 5;
     const int wm0 = (wave & 1) * (BM / 2), wn0 = (wave >> 1) * (BN / 2);
-    // this lane's places in the pair's first slot (they change sides after every pair)
+    // this lane's places in the pair's first slot
     const char* pa = smem + group * C::RING + (wn0 / 32) * 2048 + lane * 16;
     const char* pb = smem + group * C::RING + C::A_BLK * 1024 + (wm0 / 32) * 2048 + lane * 16;
-    const char* const ps = smem + group * C::RING + 4 * C::CODES + lane * 4;
-    int side = 2 * C::CODES;
-    uint32_t cur = 0;                                   // the pair's side: 0 or 1
+    const char* const ps = smem + group * C::RING + 2 * R * C::CODES + lane * 4;
+    int cur = 0;                                        // the pair's place in the ring
     auto frag_a = [&](int off, int i) { return *reinterpret_cast<const v4i*>(pa + off + i * 2048); };
     auto frag_b = [&](int off, int j) { return *reinterpret_cast<const v4i*>(pb + off + j * 2048); };
     auto scale = [&](uint32_t slot, int c) {
@@ -296,13 +299,13 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
 
     set_unit(0);
 #pragma unroll
-    for (int p = 0; p < 3; ++p) {
+    for (int p = 0; p < C::P; ++p) {
         if (p % 2 == 0) issue_scales(p / 2);
         for_each<NPAIR>([&](auto i) { issue(i, ring + (uint32_t)(p * C::CODES)); });
         next_stage();
         if (p % 2 == 1) next_pair();
     }
-    wait_vmcnt<2 * C::L + 1>();
+    wait_vmcnt<(C::P - 1) * C::L + R - 1>();
     workgroup_barrier();
     v4i fa[C::FN], fb[C::FM], ga[C::FN], gb[C::FM];
     int sa[C::FN], sb[C::FM], na[C::FN], nb[C::FM];     // the pair's scales, and the next one's
@@ -342,15 +345,15 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
             });
         }
     };
-    // One stage, of parity PAR in its pair.  It loads the stage 3 ahead into the slot
-    // of the one before it: of the pair's own first slot when odd, of the other
-    // side's second when even.  STORES: the stores of an epilogue may still be
-    // counted.
+    // One stage, of parity PAR in its pair.  It loads the stage P ahead into the slot
+    // of the one before it: the pair's own first slot when odd, the second one of the
+    // pair before when even.  `stores`: an epilogue's may still be counted.
     auto stage = [&](auto first, auto par, bool stores) {
         constexpr int PAR = decltype(par)::value;
-        const uint32_t at = ring + (PAR ? cur : cur ^ 1u) * (2 * C::CODES) + (PAR ? 0 : C::CODES);
+        const int next = cur + 1 == R ? 0 : cur + 1, before = cur == 0 ? R - 1 : cur - 1;
+        const uint32_t at = ring + (uint32_t)((PAR ? cur : before) * (2 * C::CODES) + (PAR ? 0 : C::CODES));
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (PAR == 1) issue_scales(cur);
+        if constexpr (PAR == 1) issue_scales((uint32_t)cur);
 #pragma unroll
         for (int k = 0; k < STEPS; ++k) {
             if (k < NMF) mfma_step(k, std::integral_constant<int, 2 * PAR>{}, fa, fb, decltype(first)::value);
@@ -362,20 +365,19 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
         if (stores) wait_vmcnt<OUTS + NST>();
         else wait_vmcnt<OUTS>();
         workgroup_barrier();          // every wave's; the next stage is in LDS, and this one's slot is read no more
-        if constexpr (PAR == 1) pa += side, pb += side;
+        if constexpr (PAR == 1) pa += (next - cur) * (2 * C::CODES), pb += (next - cur) * (2 * C::CODES);
 #pragma unroll
         for (int k = 0; k < STEPS; ++k) {
             if (k < NMF) mfma_step(k, std::integral_constant<int, 2 * PAR + 1>{}, ga, gb, false);
             read_step(k, PAR ? 0 : C::CODES, fa, fb);
-            if constexpr (PAR == 1) read_scale(k, cur ^ 1u);
+            if constexpr (PAR == 1) read_scale(k, (uint32_t)next);
             spread(k, std::integral_constant<int, H0>{}, std::integral_constant<int, NPAIR>{}, at);
             __builtin_amdgcn_sched_barrier(0);
         }
         next_stage();
         if constexpr (PAR == 0) next_pair();
         else {
-            side = -side;
-            cur ^= 1u;
+            cur = next;
 #pragma unroll
             for (int i = 0; i < C::FN; ++i) sa[i] = na[i];
 #pragma unroll
@@ -584,14 +586,14 @@ __global__ __launch_bounds__(256) void mx4_join_kernel(const float* __restrict__
 template <int BM, int BN, int GROUPS>
 hipError_t launch(Args g, int num_cu, hipStream_t st)
 {
-    const bool part = g.splits > 1, extra = g.ex.bias || g.ex.res;
+    const bool extra = g.ex.bias || g.ex.res;
     g.tiles_m = (g.M + BM - 1) / BM;
     g.tiles_n = (g.N + BN - 1) / BN;
     g.group_m = std::min(g.tiles_m, 4);
     const int units = g.tiles_m * g.tiles_n * g.splits;
     const dim3 grid(GROUPS > 1 ? units : std::min(units, num_cu)), block(256 * GROUPS);
-    if (part)
-        mx4_gemm_kernel<BM, BN, GROUPS, true, false><<<grid, block, 0, st>>>(g);
+    if (BM == 64 && BN == 64 && g.splits > 1)
+        mx4_gemm_kernel<64, 64, 2, true, false><<<grid, block, 0, st>>>(g);
     else if (extra)
         mx4_gemm_kernel<BM, BN, GROUPS, false, true><<<grid, block, 0, st>>>(g);
     else
@@ -599,21 +601,50 @@ hipError_t launch(Args g, int num_cu, hipStream_t st)
     return hipGetLastError();
 }
 
-// How a product runs: which tiles, how many groups a workgroup, over how many splits of k.
+// How a product runs: which tiles, over how many splits of k.
 struct Plan {
-    int bm, bn, groups, splits;
+    int bm, bn, splits;
 };
+
+// Tiles and what a call on them takes in us: start + rounds (unit + pair pairs), a
+// round being a tile a CU and a pair 256 of k.  Measured: 4096 x 4096 -> 24576, 6
+// rounds of 256 x 256 tiles, 198 us (128 x 256: 226); 2048 x 4096 -> 4096 22 us on
+// 128 x 256 (128 x 128: 28, 256 x 256 on half of the CUs: 28); 1024 x 4096 -> 4096
+// 14 us on 128 x 128 (64 x 128: 19, 128 x 256: 17); 512 x 4096 -> 4096 10.2 us on 64
+// x 128 (128 x 128: 11.5, 64 x 64: 12.2); 256 x 4096 -> 4096 7.7 us on 64 x 64 (64 x
+// 128: 8.9), with k = 12288 14.5.
+struct Shape {
+    int bm, bn, groups;
+    float start, unit, pair;
+};
+constexpr Shape kShapes[] = {{256, 256, 1, 3.0f, 9.0f, 1.5f},
+                             {128, 256, 1, 4.0f, 4.0f, 0.93f},
+                             {128, 128, 2, 2.5f, 4.0f, 0.5f},
+                             {64, 128, 2, 1.5f, 3.4f, 0.33f},
+                             {64, 64, 2, 2.3f, 2.0f, 0.21f}};
 
 Plan plan_of(int64_t m, int64_t n, int64_t k, int num_cu)
 {
-    auto tiles = [&](int bm, int bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); };
     const int64_t pairs = pad_cols(k) / 256;
-    if (pairs == 1 || tiles(256, 256) >= num_cu) return {256, 256, 1, 1};
-    if (tiles(128, 128) >= num_cu / 2) return {128, 128, 2, 1};
-    Plan p{64, 64, 2, 1};
-    if (pairs >= 4) p.groups = 4;
-    while (tiles(64, 64) * p.splits * 2 <= num_cu && pairs / (p.splits * 2) >= 4) p.splits *= 2;
-    return p;
+    Plan best{};
+    double least = 0;
+    for (const Shape& c : kShapes) {
+        if (pairs < c.groups) continue;
+        const int64_t tiles = ((m + c.bm - 1) / c.bm) * ((n + c.bn - 1) / c.bn), rounds = (tiles + num_cu - 1) / num_cu;
+        const double t = c.start + (double)rounds * (c.unit + c.pair * (double)pairs);
+        if (least == 0 || t < least) best = {c.bm, c.bn, 1}, least = t;
+    }
+    // Few of the smallest tiles and a long k: the splits' partial sums cost a second
+    // launch and their way through memory, 4 to 5 us (128 x 12288 -> 4096: 13 us, in
+    // two splits 16; 129 x 32768 -> 256: 27 us, in eight 12; 256 x 12288 -> 256: 12.4
+    // and 10.7).
+    if (best.bm == 64 && best.bn == 64) {
+        const int64_t tiles = ((m + 63) / 64) * ((n + 63) / 64);
+        int s = 1;
+        while (tiles * s * 2 <= num_cu && s < 8 && pairs / (s * 2) >= 8) s *= 2;
+        if (0.21 * (double)pairs * (1.0 - 1.0 / s) > 6.5) best.splits = s;
+    }
+    return best;
 }
 
 }  // namespace mx4
@@ -638,10 +669,14 @@ hipError_t launch_mx4_gemm(const uint8_t* xc, const uint8_t* xs, const uint8_t* 
     g.splits = p.splits;
     g.out = p.splits > 1 ? workspace : y;
     if (p.splits == 1) g.ex = ex;
-    hipError_t e = p.bm == 256     ? mx4::launch<256, 256, 1>(g, num_cu, st)
-                   : p.bm == 128   ? mx4::launch<128, 128, 2>(g, num_cu, st)
-                   : p.groups == 4 ? mx4::launch<64, 64, 4>(g, num_cu, st)
-                                   : mx4::launch<64, 64, 2>(g, num_cu, st);
+    hipError_t e = hipErrorNotSupported;
+    switch (p.bm * 1000 + p.bn) {
+        case 256256: e = mx4::launch<256, 256, 1>(g, num_cu, st); break;
+        case 128256: e = mx4::launch<128, 256, 1>(g, num_cu, st); break;
+        case 128128: e = mx4::launch<128, 128, 2>(g, num_cu, st); break;
+        case 64128: e = mx4::launch<64, 128, 2>(g, num_cu, st); break;
+        default: e = mx4::launch<64, 64, 2>(g, num_cu, st); break;
+    }
     if (e != hipSuccess || p.splits == 1) return e;
     const int64_t threads = m * n / 8;
     mx4::mx4_join_kernel<<<dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, st>>>(
