@@ -63,15 +63,35 @@ __device__ __forceinline__ void load_f32(const float* p, float (&v)[8])
     *reinterpret_cast<float4*>(v + 4) = *reinterpret_cast<const float4*>(p + 4);
 }
 
-template <typename T>
-__device__ __forceinline__ void load_mod(const Mod& m, int64_t b, int64_t t, uint32_t c, bool f32, float (&v)[8])
-{
-    const int64_t at = b * m.sb + t * m.st + c;
-    if (f32)
-        load_f32(static_cast<const float*>(m.p) + at, v);
-    else
-        unpack8<T>(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(m.p) + at), v);
-}
+// A modulation's values of each chunk.  16-bit ones of short rows (U <= 2) are
+// loaded with the row itself (begin), all others where they are used: FP32 ones
+// and long rows would cost registers, and waves in flight with them.
+template <typename T, int U>
+struct ModValues {
+    static constexpr bool kEarly = U <= 2;
+    uint4 raw[kEarly ? U : 1];
+
+    __device__ __forceinline__ static int64_t at(const Mod& m, int64_t b, int64_t t) { return b * m.sb + t * m.st; }
+    __device__ __forceinline__ void begin(const Mod& m, bool f32, int64_t b, int64_t t, const uint32_t (&c)[U])
+    {
+        if constexpr (kEarly) {
+            if (m.p && !f32) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    raw[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(m.p) + at(m, b, t) + c[u]);
+            }
+        }
+    }
+    __device__ __forceinline__ void get(const Mod& m, bool f32, int64_t b, int64_t t, int u, uint32_t c, float (&v)[8]) const
+    {
+        if (f32)
+            load_f32(static_cast<const float*>(m.p) + at(m, b, t) + c, v);
+        else if constexpr (kEarly)
+            unpack8<T>(raw[u], v);
+        else
+            unpack8<T>(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(m.p) + at(m, b, t) + c), v);
+    }
+};
 
 // v -> N(v) over the row; dead chunks hold zeros and stay zeros in the sums.
 template <int TEAM, int U>
@@ -79,6 +99,15 @@ __device__ __forceinline__ void normalise(float (&v)[U][8], const bool (&live)[U
                                           const float* w, const float* b, const Params& p, float* lds, int slot)
 {
     if (kind == 0) return;
+    constexpr bool kEarly = U <= 2;   // weights on their way during the sums, where registers allow it
+    float g[kEarly ? U : 1][8], o[kEarly ? U : 1][8];
+    if constexpr (kEarly) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (w) load_f32(w + c[u], g[u]);
+            if (b) load_f32(b + c[u], o[u]);
+        }
+    }
     if (kind == 2) {
         float s = 0.0f;
 #pragma unroll
@@ -99,25 +128,28 @@ __device__ __forceinline__ void normalise(float (&v)[U][8], const bool (&live)[U
     const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(team_sum<TEAM>(ss, lds, slot + 1), p.inv_width, p.eps));
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        float g[8], o[8];
-        if (w) load_f32(w + c[u], g);
-        if (b) load_f32(b + c[u], o);
+        const int at = kEarly ? u : 0;
+        if constexpr (!kEarly) {
+            if (w) load_f32(w + c[u], g[0]);
+            if (b) load_f32(b + c[u], o[0]);
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             v[u][i] = v[u][i] * r;
-            if (w) v[u][i] = v[u][i] * g[i];
-            if (b) v[u][i] = v[u][i] + o[i];
+            if (w) v[u][i] = v[u][i] * g[at][i];
+            if (b) v[u][i] = v[u][i] + o[at][i];
         }
     }
 }
 
 // TEAM threads a row (a wave, or the workgroup), U chunks of 8 values a thread.
-template <typename T, int TEAM, int U>
+// NT: nontemporal loads and stores of the rows.
+template <typename T, int TEAM, int U, bool NT>
 __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void block_norm_kernel(Params p)
 {
-    constexpr int NT = TEAM < 256 ? 256 : TEAM;
+    constexpr int THREADS = TEAM < 256 ? 256 : TEAM;
     __shared__ float lds[TEAM > 64 ? 4 * (TEAM / 64) : 1];
-    const uint32_t row = blockIdx.x * (NT / TEAM) + threadIdx.x / TEAM;
+    const uint32_t row = blockIdx.x * (THREADS / TEAM) + threadIdx.x / TEAM;
     if (row >= p.rows) return;   // whole waves: a workgroup of one row has none of these
     const uint32_t lane = threadIdx.x & (TEAM - 1);
     const uint32_t bi = p.by_tokens.div(row);
@@ -133,10 +165,14 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void block_norm_kernel(Par
         c[u] = live[u] ? at : 0;
         rx[u] = rb[u] = make_uint4(0, 0, 0, 0);
         if (live[u]) {
-            rx[u] = *reinterpret_cast<const uint4*>(p.x + b * p.x_sb + t * p.x_st + at);
-            if (p.branch) rb[u] = *reinterpret_cast<const uint4*>(p.branch + b * p.b_sb + t * p.b_st + at);
+            rx[u] = load16<NT>(p.x + b * p.x_sb + t * p.x_st + at);
+            if (p.branch) rb[u] = load16<NT>(p.branch + b * p.b_sb + t * p.b_st + at);
         }
     }
+    ModValues<T, U> gate, scale, shift;
+    gate.begin(p.gate, p.mod32, b, t, c);
+    scale.begin(p.scale, p.mod32, b, t, c);
+    shift.begin(p.shift, p.mod32, b, t, c);
     float v[U][8];
     if (p.branch) {
 #pragma unroll
@@ -147,7 +183,7 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void block_norm_kernel(Par
             float g[8], x[8];
             unpack8<T>(rx[u], x);
             if (p.gate.p) {
-                load_mod<T>(p.gate, b, t, c[u], p.mod32, g);
+                gate.get(p.gate, p.mod32, b, t, u, c[u], g);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[u][i] = v[u][i] * g[i];
             }
@@ -156,7 +192,7 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void block_norm_kernel(Par
                 v[u][i] = __builtin_fmaf(p.branch_scale, v[u][i], p.residual_scale * x[i]);
                 if (!live[u]) v[u][i] = 0.0f;
             }
-            if (p.x_out && live[u]) *reinterpret_cast<uint4*>(p.x_out + b * p.xo_sb + t * p.xo_st + c[u]) = pack8<T>(v[u]);
+            if (p.x_out && live[u]) store16<NT>(p.x_out + b * p.xo_sb + t * p.xo_st + c[u], pack8<T>(v[u]));
         }
     } else {
 #pragma unroll
@@ -172,16 +208,16 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void block_norm_kernel(Par
     for (int u = 0; u < U; ++u) {
         float g[8];
         if (p.scale.p) {
-            load_mod<T>(p.scale, b, t, c[u], p.mod32, g);
+            scale.get(p.scale, p.mod32, b, t, u, c[u], g);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[u][i] = __builtin_fmaf(v[u][i], g[i], v[u][i]);
         }
         if (p.shift.p) {
-            load_mod<T>(p.shift, b, t, c[u], p.mod32, g);
+            shift.get(p.shift, p.mod32, b, t, u, c[u], g);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[u][i] = v[u][i] + g[i];
         }
-        if (live[u]) *reinterpret_cast<uint4*>(p.out + b * p.o_sb + t * p.o_st + c[u]) = pack8<T>(v[u]);
+        if (live[u]) store16<NT>(p.out + b * p.o_sb + t * p.o_st + c[u], pack8<T>(v[u]));
     }
 }
 
@@ -189,22 +225,32 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void block_norm_kernel(Par
 
 namespace {
 
-template <typename T, int TEAM, int U>
+template <typename T, int TEAM, int U, bool NT>
 hipError_t launch(const bnorm::Params& p, hipStream_t st)
 {
     constexpr uint32_t nt = TEAM < 256 ? 256 : TEAM, per = nt / TEAM;
-    bnorm::block_norm_kernel<T, TEAM, U><<<dim3((p.rows + per - 1) / per), dim3(nt), 0, st>>>(p);
+    bnorm::block_norm_kernel<T, TEAM, U, NT><<<dim3((p.rows + per - 1) / per), dim3(nt), 0, st>>>(p);
     return hipGetLastError();
 }
 
+template <typename T, bool NT>
+hipError_t pick_team(const bnorm::Params& p, hipStream_t st)
+{
+    if (p.width <= 512) return launch<T, 64, 1, NT>(p, st);
+    if (p.width <= 1536 && p.rows >= 16u * (uint32_t)num_cus())
+        return p.width <= 1024 ? launch<T, 64, 2, NT>(p, st) : launch<T, 64, 3, NT>(p, st);
+    if (p.width <= 2048) return launch<T, 256, 1, NT>(p, st);
+    if (p.width <= 4096) return launch<T, 256, 2, NT>(p, st);
+    if (p.width <= 8192) return launch<T, 256, 4, NT>(p, st);
+    return launch<T, 256, 8, NT>(p, st);
+}
+
+// Rows past the Infinity Cache go by nontemporal loads and stores.
 template <typename T>
 hipError_t pick(const bnorm::Params& p, hipStream_t st)
 {
-    if (p.width <= 512) return launch<T, 64, 1>(p, st);
-    if (p.width <= 2048) return launch<T, 256, 1>(p, st);
-    if (p.width <= 4096) return launch<T, 256, 2>(p, st);
-    if (p.width <= 8192) return launch<T, 256, 4>(p, st);
-    return launch<T, 256, 8>(p, st);
+    const int64_t bytes = (int64_t)p.rows * p.width * 8;
+    return bytes < kInfinityCacheBytes ? pick_team<T, false>(p, st) : pick_team<T, true>(p, st);
 }
 
 bnorm::Mod mod_of(const ModArgs& m) { return bnorm::Mod{m.p, m.sb, m.st}; }

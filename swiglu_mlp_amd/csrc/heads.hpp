@@ -15,6 +15,23 @@ typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 // run slower.
 constexpr int64_t kInfinityCacheBytes = 256 << 20;
 
+// 16 bytes, nontemporal or not.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+template <bool NT>
+__device__ __forceinline__ uint4 load16(const uint16_t* p)
+{
+    if constexpr (NT) return __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p)));
+    return *reinterpret_cast<const uint4*>(p);
+}
+template <bool NT>
+__device__ __forceinline__ void store16(uint16_t* p, uint4 v)
+{
+    if constexpr (NT)
+        __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4*>(p));
+    else
+        *reinterpret_cast<uint4*>(p) = v;
+}
+
 // n / d for n < 2^31 and 1 <= d < 2^31 as one high product and a shift, after
 // Granlund and Montgomery, "Division by invariant integers using
 // multiplication" (1994): with s = ceil(log2 d) - 1 and m = floor(2^(32+s) / d)

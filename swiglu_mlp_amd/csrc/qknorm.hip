@@ -37,22 +37,6 @@ struct Side {
     FastDiv by_hg, by_tokens;
 };
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-template <bool NT>
-__device__ __forceinline__ uint4 load16(const uint16_t* p)
-{
-    if constexpr (NT) return __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p)));
-    return *reinterpret_cast<const uint4*>(p);
-}
-template <bool NT>
-__device__ __forceinline__ void store16(uint16_t* p, uint4 v)
-{
-    if constexpr (NT)
-        __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4*>(p));
-    else
-        *reinterpret_cast<uint4*>(p) = v;
-}
-
 template <int TEAM>
 __device__ __forceinline__ float team_sum(float v)
 {
