@@ -490,8 +490,10 @@ size_t ck_mx4_gemm_workspace_size(int64_t m, int64_t k, int64_t n);
 
 /* The MX FP4 linear: ck_mx4_act_quant of x into the workspace, then
  * ck_mx4_gemm_bf16.  Arguments as there, the weight in CK_LAYOUT_BLOCKED.
- *   workspace  ck_mx4_linear_workspace_size(m, k, n) bytes, 256-byte aligned,
- *              clobbered; apart from every other buffer of the call
+ *   workspace  ck_mx4_linear_workspace_size(m, k, n) bytes (0: may be NULL),
+ *              256-byte aligned, clobbered; apart from every other buffer of the
+ *              call.  While m * k, k padded to 256, is at most 16384 (and m at
+ *              most 16) one kernel quantizes the rows itself and needs none.
  * Errors as ck_int8_linear. */
 ck_status ck_mx4_linear(const uint16_t *x, int64_t ldx, int32_t act, const uint8_t *w_codes,
                         const uint8_t *w_scales, const float *bias, const uint16_t *residual,

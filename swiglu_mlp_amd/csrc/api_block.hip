@@ -128,10 +128,11 @@ ck_status ck_mx4_gemm_bf16(const uint8_t* x_codes, const uint8_t* x_scales, cons
                                         ck::EpiExtra{bias, residual}, workspace, (hipStream_t)stream));
 }
 
-// The activation's codes, its scales, then the product's workspace.
+// The activation's codes, its scales, then the product's workspace; nothing where
+// the quantizer is inside the product.
 size_t ck_mx4_linear_workspace_size(int64_t m, int64_t k, int64_t n)
 {
-    if (m <= 0 || n <= 0 || check_product(m, n, k, 1) != CK_OK) return 0;
+    if (m <= 0 || n <= 0 || check_product(m, n, k, 1) != CK_OK || ck::mx4_fused(m, k)) return 0;
     return round_up(codes_bytes(m, k)) + round_up(scales_bytes(m, k)) + ck_mx4_gemm_workspace_size(m, k, n);
 }
 
@@ -146,7 +147,7 @@ ck_status ck_mx4_linear(const uint16_t* x, int64_t ldx, int32_t act, const uint8
     CK_TRY(check_epilogue(bias, residual, y));
     if (!good_workspace(workspace, workspace_bytes, ck_mx4_linear_workspace_size(m, k, n))) return CK_EWORKSPACE;
     hipStream_t st = (hipStream_t)stream;
-    if (ck::mx4_fused(m, k))   // the quantizer inside the product: one launch, the workspace untouched
+    if (ck::mx4_fused(m, k))   // the quantizer inside the product: one launch, no workspace
         return from_hip(ck::launch_mx4_fused(act == CK_ACT_SWIGLU ? 1 : 0, x, ldx, w_codes, w_scales, m, n, k, group, y,
                                              ck::EpiExtra{bias, residual}, st));
     uint8_t* xc = static_cast<uint8_t*>(workspace);

@@ -32,9 +32,10 @@ __device__ __forceinline__ uint32_t scale_byte(float a)
 // 2^(byte - 127), byte < 255 (2^-127 is a subnormal).
 __device__ __forceinline__ float scale_value(uint32_t byte) { return __uint_as_float(max(byte << 23, 0x00400000u)); }
 
-// silu(g) * u for the quantizer: the hardware's exponential and reciprocal are
-// within 2^-22 of the result, far below half a step of a 4-bit value.  g = -inf
-// gives NaN (-inf * 0), a large negative g -0.
+// silu(g) * u for the quantizer.  The hardware's exponential and reciprocal and the
+// rounding of g log2(e) leave it within (4 + |g|) 2^-24 of itself for negative g
+// (4 2^-24 for positive), far below half a step of a 4-bit value.  g = -inf gives
+// NaN (-inf * 0), a large negative g -0.
 __device__ __forceinline__ float silu_mul(float g, float u)
 {
     return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -0x1.715476p+0f)) * u;

@@ -94,9 +94,11 @@ def test_mx4_products(L):
                      ({"act": 1, "ld": 256}, ESHAPE), ({"act": 3}, EINVAL), ({"group": 5}, EUNSUP),
                      ({"k": 320, "group": 128}, ESHAPE)):
         assert lin(**kw) == want, kw
-    need = L.ck_mx4_linear_workspace_size(8, 256, 64)
+    assert L.ck_mx4_linear_workspace_size(8, 256, 64) == 0      # few rows: one kernel, no workspace
+    need = L.ck_mx4_linear_workspace_size(40, 4096, 64)
+    assert need > 0
     for kw in ({"room": None}, {"size": need - 1}, {"room": FAKE + 16}):
-        assert lin(**kw) == EWS
+        assert lin(m=40, k=4096, **kw) == EWS
     need = L.ck_mx4_gemm_workspace_size(100, 16384, 512)
     for kw in ({"room": None}, {"size": need - 1}, {"room": FAKE + 16}):
         if need:

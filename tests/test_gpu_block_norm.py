@@ -313,3 +313,33 @@ def test_refusals_of_shared_memory():
                dict(out=buf.as_strided((2, 3, 64), (192, 32, 1), 1 << 13))):
         with pytest.raises(ValueError):
             ck.ck_block_norm(x, y, **kw)
+
+
+# ---------------------------------------------------------------- a block of norms, 4-bit linears and attention
+def test_block_of_norms_linears_and_attention():
+    """The example block against FP32 with unquantized weights.  Either operand of a 4-bit linear is a value's last step
+    off at most: a relative (1/4) / sqrt(3) = 0.144 as a root mean square, sqrt(2) times that with both.  A branch has two
+    linears in a row with a softmax' average or a product of halves between them: 2 x 0.204 of its size.  The sum of the
+    branches' errors, each of its gated size, bounds the block's; and a block without its branches is further off."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    from examples import gated_block as gb
+    weights, x, modulation, rope = gb.synthetic(b=3, t=70, heads=4, d=64, inner=512)
+    kept = x.clone()
+    block = gb.GatedBlock(weights, 4)
+    y = block(x, modulation, rope)
+    assert torch.equal(x, kept)
+    want, first, second = gb.reference(weights, 4, x, modulation, rope)
+    off = (y.float() - want).norm()
+    bound = 2 * math.sqrt(2) * 0.25 / math.sqrt(3) * (first.norm() + second.norm()) + U[BF16] * 3 * want.norm()
+    say(f"block: off {off.item():.3f}, bound {bound.item():.3f}, branches {(first + second).norm().item():.3f}")
+    assert off < bound and off < (first + second).norm()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        z = block(x, modulation, rope)
+    for _ in range(3):
+        z.fill_(0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(z, y) and torch.equal(block(x, modulation, rope), y)

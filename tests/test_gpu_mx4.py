@@ -8,7 +8,9 @@ Bounds elsewhere, u = 2^-8 the largest relative error of a rounding to BF16:
   rotated values  group sums of FP32 numbers: log2(group) roundings of partial sums
                   that |a|'s sum bounds and one product, so within
                   t = (log2(group) + 2) 2^-24 sum |a| / sqrt(group); with SwiGLU
-                  each a is 2^-21 |a| off before that.  A code is then the
+                  each a is 4 2^-24 |a| off before that, and for a negative gate g
+                  another |g| 2^-24 |a|: under 2^-21 |a| in all down to g = -4, and below
+                  that |a| < |u| / 13 falls faster than |g| grows.  A code is then the
                   nearest of values within t, and a scale that of such a maximum.
   product         every one of the k products is exact in FP32 and passes at most 64
                   roundings in its instruction and one in each of the k / 64
@@ -441,12 +443,15 @@ def test_refusals():
     no(lin, x.float(), *wb), no(lin, x, *wb, group=0), no(lin, x, *wb, n=40), no(lin, x, wb[0], wb[0])
     no(lin, x[:, :128], *wp(torch.randn(48, 512, device=DEV), 64), group=64), no(lin, x, *wb, bias=torch.zeros(48, device=DEV))
     no(lin, x, *wb, bias=torch.zeros(64, device=DEV).to(BF16)), no(lin, x, *wb, residual=torch.zeros(4, 48, dtype=BF16, device=DEV))
-    no(lin, x, *wb, out=torch.zeros(4, 64, device=DEV)), no(lin, x, *wb, workspace=torch.zeros(16, dtype=torch.uint8, device=DEV))
+    no(lin, x, *wb, out=torch.zeros(4, 64, device=DEV)), 
+    wide = activation(40, 4096, 1)
+    w4 = ck.ck_mx4_weight_prep(torch.randn(48, 4096, device=DEV), 64)
+    no(lin, wide, *w4, group=64, workspace=torch.zeros(16, dtype=torch.uint8, device=DEV))
     no(lin, x.cpu(), *wb), no(lin, x, wb[0].cpu(), wb[1]), no(lin, x, *wb, input_act="relu")
 
 
 def test_refusals_of_shared_memory():
-    k, n, m = 256, 64, 8
+    k, n, m = 256, 64, 72           # (too many rows for one kernel without a workspace)
     need = ck.lib().ck_mx4_linear_workspace_size(m, k, n)
     buf = torch.zeros(1 << 20, dtype=torch.uint8, device=DEV)
 
@@ -454,14 +459,14 @@ def test_refusals_of_shared_memory():
         size = math.prod(shape) * torch.empty(0, dtype=dtype).element_size()
         return buf[at:at + size].view(dtype).view(*shape)
 
-    x, y = part(0, BF16, m, k), part(1 << 14, BF16, m, n)
+    x, y = part(1 << 19, BF16, m, k), part(1 << 14, BF16, m, n)
     wc, ws = part(1 << 15, torch.uint8, 2, 4, 1024), part(1 << 16, torch.uint8, 2, 1, 256)
     room, bias = buf[1 << 18:(1 << 18) + need], part(1 << 17, torch.float32, n)
     kw = dict(group=64, bias=bias)
     ck.ck_mx4_linear(x, wc, ws, out=y, workspace=room, **kw)
-    for bad in ({"out": part(m * k * 2 - 16, BF16, m, n)}, {"out": part((1 << 15) - 16, BF16, m, n)},
+    for bad in ({"out": part((1 << 19) + m * k * 2 - 16, BF16, m, n)}, {"out": part((1 << 15) - 16, BF16, m, n)},
                 {"out": part((1 << 16) + 256, BF16, m, n)}, {"out": part(1 << 17, BF16, m, n)},
-                {"residual": part((1 << 14) + 16, BF16, m, n), "out": y}, {"workspace": buf[:need]},
+                {"residual": part((1 << 14) + 16, BF16, m, n), "out": y}, {"workspace": buf[(1 << 19) - 256:(1 << 19) - 256 + need]},
                 {"workspace": buf[1 << 14:(1 << 14) + need], "out": y}, {"workspace": buf[(1 << 18) + 16:(1 << 18) + 16 + need]},
                 {"workspace": buf[1 << 17:(1 << 17) + need]}):
         with pytest.raises(ValueError):
