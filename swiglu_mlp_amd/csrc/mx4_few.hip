@@ -12,7 +12,8 @@
 //
 // FUSED: while the weight's loads are in flight the workgroup quantizes the rows
 // of x itself, into LDS, so the call is one launch; every workgroup repeats that,
-// so only while it is one block of 32 values a thread (rows * k <= 16384).
+// so only while it is one block of 32 values a thread (rows * k <= 16384): one token
+// 4096 -> 12288, 26.7 MB of weight, 7.0 us (16 tokens, quantized before: 4.2 + 6.6).
 #include "ck_internal.hpp"
 #include "mx4.hpp"
 
@@ -240,10 +241,15 @@ hipError_t launch_few(const FewArgs& g, hipStream_t st)
 
 }  // namespace mx4
 
-bool mx4_few_rows(int64_t m, int64_t n, int64_t)
+// Up to 32 rows always; up to 128 of a narrow weight (one workgroup a CU) and of a k
+// that the waves get through before the tiles' second launch pays, whose operands
+// are shared by more rows.  Measured, this kernel and the tiles: 32 x 2048 -> 24576
+// 6.6 and 8.2 us, 128 x 4096 -> 4096 5.9 and 7.0, 128 x 12288 -> 4096 12.5 and 13.0,
+// 128 x 16384 -> 1024 14.0 and 11.7, 64 x 32768 -> 4096 22.9 and 19.0, 33 x 4096 ->
+// 8176 8.2 and 7.1.
+bool mx4_few_rows(int64_t m, int64_t n, int64_t k)
 {
-    const int64_t cus = num_cus();
-    return m <= 32 || (m <= 64 && n < 32 * cus) || (m <= 128 && n <= 16 * cus);
+    return m <= 32 || (m <= 128 && n <= 16 * num_cus() && m * k <= 3 << 19);
 }
 
 hipError_t launch_mx4_few(const uint8_t* xc, const uint8_t* xs, const uint8_t* wc, const uint8_t* ws, int64_t m, int64_t n,
