@@ -347,36 +347,43 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
     };
     // One stage, of parity PAR in its pair.  It loads the stage P ahead into the slot
     // of the one before it: the pair's own first slot when odd, the second one of the
-    // pair before when even.  `stores`: an epilogue's may still be counted.
-    auto stage = [&](auto first, auto par, bool stores) {
-        constexpr int PAR = decltype(par)::value;
+    // pair before when even.  `stores`: an epilogue's may still be counted.  LEFT: the
+    // stages after it, 3 for more than that; the last three load nothing.
+    auto stage = [&](auto first, auto par, auto left, bool stores) {
+        constexpr int PAR = decltype(par)::value, LEFT = decltype(left)::value;
         const int next = cur + 1 == R ? 0 : cur + 1, before = cur == 0 ? R - 1 : cur - 1;
         const uint32_t at = ring + (uint32_t)((PAR ? cur : before) * (2 * C::CODES) + (PAR ? 0 : C::CODES));
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (PAR == 1) issue_scales((uint32_t)cur);
+        if constexpr (PAR == 1 && LEFT == 3) issue_scales((uint32_t)cur);
 #pragma unroll
         for (int k = 0; k < STEPS; ++k) {
             if (k < NMF) mfma_step(k, std::integral_constant<int, 2 * PAR>{}, fa, fb, decltype(first)::value);
             read_step(k, PAR * C::CODES + 1024, ga, gb);
-            spread(k, std::integral_constant<int, 0>{}, std::integral_constant<int, H0>{}, at);
+            if constexpr (LEFT == 3) spread(k, std::integral_constant<int, 0>{}, std::integral_constant<int, H0>{}, at);
             __builtin_amdgcn_sched_barrier(0);
         }
-        wait_lgkmcnt0();              // this wave's fragments of the second half are in registers
-        if (stores) wait_vmcnt<OUTS + NST>();
-        else wait_vmcnt<OUTS>();
-        workgroup_barrier();          // every wave's; the next stage is in LDS, and this one's slot is read no more
-        if constexpr (PAR == 1) pa += (next - cur) * (2 * C::CODES), pb += (next - cur) * (2 * C::CODES);
+        if constexpr (LEFT > 0) {
+            wait_lgkmcnt0();          // this wave's fragments of the second half are in registers
+            if constexpr (LEFT == 1) wait_vmcnt<0>();
+            else if constexpr (LEFT == 2) wait_vmcnt<C::L>();   // of the last stage
+            else if (stores) wait_vmcnt<OUTS + NST>();
+            else wait_vmcnt<OUTS>();
+            workgroup_barrier();      // every wave's; the next stage is in LDS, and this one's slot is read no more
+        }
+        if constexpr (PAR == 1 && LEFT > 0) pa += (next - cur) * (2 * C::CODES), pb += (next - cur) * (2 * C::CODES);
 #pragma unroll
         for (int k = 0; k < STEPS; ++k) {
             if (k < NMF) mfma_step(k, std::integral_constant<int, 2 * PAR + 1>{}, ga, gb, false);
-            read_step(k, PAR ? 0 : C::CODES, fa, fb);
-            if constexpr (PAR == 1) read_scale(k, (uint32_t)next);
-            spread(k, std::integral_constant<int, H0>{}, std::integral_constant<int, NPAIR>{}, at);
+            if constexpr (LEFT > 0) read_step(k, PAR ? 0 : C::CODES, fa, fb);
+            if constexpr (PAR == 1 && LEFT > 0) read_scale(k, (uint32_t)next);
+            if constexpr (LEFT == 3) spread(k, std::integral_constant<int, H0>{}, std::integral_constant<int, NPAIR>{}, at);
             __builtin_amdgcn_sched_barrier(0);
         }
-        next_stage();
-        if constexpr (PAR == 0) next_pair();
-        else {
+        if constexpr (LEFT == 3) {
+            next_stage();
+            if constexpr (PAR == 0) next_pair();
+        }
+        if constexpr (PAR == 1 && LEFT > 0) {
             cur = next;
 #pragma unroll
             for (int i = 0; i < C::FN; ++i) sa[i] = na[i];
@@ -484,26 +491,37 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
         }
     };
 
-    constexpr std::integral_constant<int, 0> even{};
-    constexpr std::integral_constant<int, 1> odd{};
+    constexpr std::integral_constant<int, 0> even{}, last{};
+    constexpr std::integral_constant<int, 1> odd{}, one_left{};
+    constexpr std::integral_constant<int, 2> two_left{};
+    constexpr std::integral_constant<int, 3> more{};
+    constexpr std::true_type first{};
+    constexpr std::false_type later{};
     if constexpr (GROUPS == 1) {
         for (int q = 0; q < my_units; ++q) {
-            stage(std::true_type{}, even, q > 0);
-            stage(std::false_type{}, odd, q > 0);
+            stage(first, even, more, q > 0);
+            stage(later, odd, more, q > 0);
             for (int p = 1; p < pairs; ++p) {
-                stage(std::false_type{}, even, false);
-                stage(std::false_type{}, odd, false);
+                stage(later, even, more, false);
+                stage(later, odd, more, false);
             }
             epilogue(unit_of(q), 0, C::FM);
         }
         wait_vmcnt<0>();   // no LDS load may land after the workgroup retires
     } else {
-        stage(std::true_type{}, even, false);
-        stage(std::false_type{}, odd, false);
-        for (int p = 1; p < pairs; ++p) {
-            stage(std::false_type{}, even, false);
-            stage(std::false_type{}, odd, false);
+        // (of one pair only the prologue's third stage is loaded for nothing)
+        if (pairs == 1) {
+            stage(first, even, one_left, false);
+        } else {
+            stage(first, even, more, false);
+            for (int p = 2; p < pairs; ++p) {
+                stage(later, odd, more, false);
+                stage(later, even, more, false);
+            }
+            stage(later, odd, two_left, false);
+            stage(later, even, one_left, false);
         }
+        stage(later, odd, last, false);
         if (pairs < most_pairs) {   // as many barriers in every group
             workgroup_barrier();
             workgroup_barrier();
