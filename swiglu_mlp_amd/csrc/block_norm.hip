@@ -9,6 +9,9 @@
 // read once and r and h written once: 8 bytes a value, which is what bounds it.
 // All steps are FP32 and h is computed from the unrounded r; the variance is that
 // of the centred values (a second sum over registers), not a difference of sums.
+//
+// 65536 rows of 4096 with two RMS norms, 2.1 GB: 387 us (5.5 TB/s); 8192 rows with
+// three modulations a sequence, 268 MB, 51 us (5.3); 16 rows 2.7 to 4 us, a launch.
 #include "ck_internal.hpp"
 #include "heads.hpp"
 
@@ -233,6 +236,11 @@ hipError_t launch(const bnorm::Params& p, hipStream_t st)
     return hipGetLastError();
 }
 
+// A workgroup a row, so that the row's bytes are in flight at once from many lanes;
+// a wave a row (no barriers between the sums, less to wait for) where many rows are
+// narrow.  Measured, wave and workgroup: 16384 rows of 1160 39 and 43 us, 4096 of
+// them 11.4 and 12.2, 1024 5.8 and 5.9, 16 4.9 and 3.7; 16384 rows of 2048 51 and 46;
+// 4096 rows of 4096 34 and 28 (248 registers a lane).
 template <typename T, bool NT>
 hipError_t pick_team(const bnorm::Params& p, hipStream_t st)
 {
@@ -245,7 +253,8 @@ hipError_t pick_team(const bnorm::Params& p, hipStream_t st)
     return launch<T, 256, 8, NT>(p, st);
 }
 
-// Rows past the Infinity Cache go by nontemporal loads and stores.
+// Rows past the Infinity Cache go by nontemporal loads and stores: 65536 rows of
+// 4096 387 us for 403, 32768 of 8192 388 for 405; 4096 of 4096 (134 MB) 29 for 28.
 template <typename T>
 hipError_t pick(const bnorm::Params& p, hipStream_t st)
 {
