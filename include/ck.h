@@ -479,7 +479,8 @@ ck_status ck_mx4_dequant(const uint8_t *codes, const uint8_t *scales, int64_t ro
 
 /* y[m, n] = bf16(sum_k x[m, k] w[n, k] (+ bias[n]) (+ residual[m, n])), operands
  * in CK_LAYOUT_BLOCKED, sums in FP32 in a fixed order (the same call gives the
- * same bits), one rounding at the end.  bias, residual and y as ck_int8_linear.
+ * same bits), one rounding at the end.  bias, residual and y as ck_int8_linear,
+ * the residual 16-byte aligned.
  *   workspace  ck_mx4_gemm_workspace_size(m, k, n) bytes (0: may be NULL),
  *              256-byte aligned, clobbered */
 ck_status ck_mx4_gemm_bf16(const uint8_t *x_codes, const uint8_t *x_scales, const uint8_t *w_codes,
