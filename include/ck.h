@@ -480,14 +480,10 @@ ck_status ck_mx4_dequant(const uint8_t *codes, const uint8_t *scales, int64_t ro
 /* y[m, n] = bf16(sum_k x[m, k] w[n, k] (+ bias[n]) (+ residual[m, n])), operands
  * in CK_LAYOUT_BLOCKED, sums in FP32 in a fixed order (the same call gives the
  * same bits), one rounding at the end.  bias, residual and y as ck_int8_linear,
- * the residual 16-byte aligned.
- *   workspace  ck_mx4_gemm_workspace_size(m, k, n) bytes (0: may be NULL),
- *              256-byte aligned, clobbered */
+ * the residual 16-byte aligned. */
 ck_status ck_mx4_gemm_bf16(const uint8_t *x_codes, const uint8_t *x_scales, const uint8_t *w_codes,
                            const uint8_t *w_scales, const float *bias, const uint16_t *residual,
-                           int64_t m, int64_t n, int64_t k, uint16_t *y, void *workspace,
-                           size_t workspace_bytes, void *stream);
-size_t ck_mx4_gemm_workspace_size(int64_t m, int64_t k, int64_t n);
+                           int64_t m, int64_t n, int64_t k, uint16_t *y, void *stream);
 
 /* The MX FP4 linear: ck_mx4_act_quant of x into the workspace, then
  * ck_mx4_gemm_bf16.  Arguments as there, the weight in CK_LAYOUT_BLOCKED.

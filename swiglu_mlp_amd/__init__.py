@@ -123,7 +123,7 @@ def bind(path: str) -> ctypes.CDLL:
         "ck_mx4_weight_pack": [p, p, i64, i64, p, p, p],
         "ck_mx4_act_quant": [p, i64, i64, i64, i32, i32, i32, p, p, p],
         "ck_mx4_dequant": [p, p, i64, i64, i32, p, p],
-        "ck_mx4_gemm_bf16": [p, p, p, p, p, p, i64, i64, i64, p, p, sz, p],
+        "ck_mx4_gemm_bf16": [p, p, p, p, p, p, i64, i64, i64, p, p],
         "ck_mx4_linear": [p, i64, i32, p, p, p, p, i64, i64, i64, i32, p, p, sz, p],
         "ck_block_norm": [p, p],
         "ck_silu_f32": [p, i64, p, p],
@@ -145,9 +145,8 @@ def bind(path: str) -> ctypes.CDLL:
     L.ck_swiglu_mlp_workspace_size.restype = sz
     L.ck_cross_attn_workspace_size.argtypes = [i64] * 7
     L.ck_cross_attn_workspace_size.restype = sz
-    for f in (L.ck_mx4_gemm_workspace_size, L.ck_mx4_linear_workspace_size):
-        f.argtypes = [i64, i64, i64]
-        f.restype = sz
+    L.ck_mx4_linear_workspace_size.argtypes = [i64, i64, i64]
+    L.ck_mx4_linear_workspace_size.restype = sz
     for f in (L.ck_mx4_rows, L.ck_mx4_cols):
         f.argtypes = [i64]
         f.restype = i64
@@ -705,8 +704,8 @@ def _native():
                               "with `python -m swiglu_mlp_amd.build`") from e
         m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
                  for f in (L.ck_qk_norm_rope, L.ck_cross_attn, L.ck_cross_attn_workspace_size, L.ck_mx4_weight_prep,
-                           L.ck_mx4_act_quant, L.ck_mx4_dequant, L.ck_mx4_gemm_bf16, L.ck_mx4_gemm_workspace_size,
-                           L.ck_mx4_linear, L.ck_mx4_linear_workspace_size, L.ck_block_norm)),
+                           L.ck_mx4_act_quant, L.ck_mx4_dequant, L.ck_mx4_gemm_bf16, L.ck_mx4_linear,
+                           L.ck_mx4_linear_workspace_size, L.ck_block_norm)),
                torch._C._cuda_getCurrentRawStream)
         _calls = m
     return _calls
@@ -810,12 +809,12 @@ def ck_mx4_dequant(codes, scales, rows: int | None = None, k: int | None = None)
     return _done("ck_mx4_dequant", (_calls or _native()).mx4_dequant(codes, scales, rows, k))
 
 
-def ck_mx4_gemm_bf16(x_codes, x_scales, w_codes, w_scales, m: int, n: int | None = None, out=None, workspace=None,
-                     bias=None, residual=None):
+def ck_mx4_gemm_bf16(x_codes, x_scales, w_codes, w_scales, m: int, n: int | None = None, out=None, bias=None,
+                     residual=None):
     """y = bf16(x w^T (+ bias) (+ residual)) of blocked 4-bit operands with m and
     n logical rows (n default: the weight's padded rows)."""
     return _done("ck_mx4_gemm_bf16", (_calls or _native()).mx4_gemm(x_codes, x_scales, w_codes, w_scales, m, n, bias,
-                                                                   residual, out, workspace))
+                                                                   residual, out))
 
 
 def ck_mx4_linear(x, w_codes, w_scales, n: int | None = None, group: int = 128, input_act=None, out=None,

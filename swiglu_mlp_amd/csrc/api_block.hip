@@ -12,7 +12,7 @@ namespace {
 
 constexpr int64_t kMaxValues = 1LL << 34;     // of an operand, padded: launches below 2^32 threads
 constexpr int64_t kMaxOutputs = 1LL << 35;    // m * n
-constexpr int64_t kMaxFeatures = 1LL << 21;   // 256 rows of FP32 sums in 32-bit offsets
+constexpr int64_t kMaxFeatures = 1LL << 21;   // a tile's 256 rows of y in 31-bit offsets
 
 size_t codes_bytes(int64_t rows, int64_t k) { return (size_t)(ck::mx4::pad_rows(rows) * ck::mx4::pad_cols(k) / 2); }
 size_t scales_bytes(int64_t rows, int64_t k) { return (size_t)(ck::mx4::pad_rows(rows) * ck::mx4::pad_cols(k) / 32); }
@@ -107,15 +107,9 @@ ck_status ck_mx4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t ro
                                            (hipStream_t)stream));
 }
 
-size_t ck_mx4_gemm_workspace_size(int64_t m, int64_t k, int64_t n)
-{
-    if (m <= 0 || n <= 0 || check_product(m, n, k, 1) != CK_OK) return 0;
-    return round_up(ck::mx4_gemm_workspace(m, n, k));
-}
-
 ck_status ck_mx4_gemm_bf16(const uint8_t* x_codes, const uint8_t* x_scales, const uint8_t* w_codes,
                            const uint8_t* w_scales, const float* bias, const uint16_t* residual, int64_t m, int64_t n,
-                           int64_t k, uint16_t* y, void* workspace, size_t workspace_bytes, void* stream)
+                           int64_t k, uint16_t* y, void* stream)
 {
     CK_TRY(check_product(m, n, k, 1));
     if (m == 0 || n == 0) return CK_OK;
@@ -123,17 +117,16 @@ ck_status ck_mx4_gemm_bf16(const uint8_t* x_codes, const uint8_t* x_scales, cons
         !aligned16(w_codes) || !aligned16(w_scales))
         return CK_EINVAL;
     CK_TRY(check_epilogue(bias, residual, y));
-    if (!good_workspace(workspace, workspace_bytes, ck_mx4_gemm_workspace_size(m, k, n))) return CK_EWORKSPACE;
     return from_hip(ck::launch_mx4_gemm(x_codes, x_scales, w_codes, w_scales, m, n, k, y,
-                                        ck::EpiExtra{bias, residual}, workspace, (hipStream_t)stream));
+                                        ck::EpiExtra{bias, residual}, (hipStream_t)stream));
 }
 
-// The activation's codes, its scales, then the product's workspace; nothing where
-// the quantizer is inside the product.
+// The activation's codes, then its scales; nothing where the quantizer is inside the
+// product.
 size_t ck_mx4_linear_workspace_size(int64_t m, int64_t k, int64_t n)
 {
     if (m <= 0 || n <= 0 || check_product(m, n, k, 1) != CK_OK || ck::mx4_fused(m, k)) return 0;
-    return round_up(codes_bytes(m, k)) + round_up(scales_bytes(m, k)) + ck_mx4_gemm_workspace_size(m, k, n);
+    return round_up(codes_bytes(m, k)) + round_up(scales_bytes(m, k));
 }
 
 ck_status ck_mx4_linear(const uint16_t* x, int64_t ldx, int32_t act, const uint8_t* w_codes, const uint8_t* w_scales,
@@ -153,8 +146,7 @@ ck_status ck_mx4_linear(const uint16_t* x, int64_t ldx, int32_t act, const uint8
     uint8_t* xc = static_cast<uint8_t*>(workspace);
     uint8_t* xs = xc + round_up(codes_bytes(m, k));
     CK_TRY(from_hip(ck::launch_mx4_quant(act == CK_ACT_SWIGLU ? 1 : 0, x, ldx, m, k, group, true, xc, xs, st)));
-    return from_hip(ck::launch_mx4_gemm(xc, xs, w_codes, w_scales, m, n, k, y, ck::EpiExtra{bias, residual},
-                                        xs + round_up(scales_bytes(m, k)), st));
+    return from_hip(ck::launch_mx4_gemm(xc, xs, w_codes, w_scales, m, n, k, y, ck::EpiExtra{bias, residual}, st));
 }
 
 // ---- between two sub-blocks ----

@@ -160,16 +160,15 @@ hipError_t launch_mx4_dequant(const uint8_t* codes, const uint8_t* scales, int64
                               uint16_t* out, hipStream_t st);
 
 // y = bf16(x . w^T (+ bias) (+ residual)) of blocked 4-bit operands
-// (mx4_gemm.hip); workspace of mx4_gemm_workspace bytes (0: unused).
-size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k);
+// (mx4_gemm.hip).
 hipError_t launch_mx4_gemm(const uint8_t* xc, const uint8_t* xs, const uint8_t* wc, const uint8_t* ws, int64_t m,
-                           int64_t n, int64_t k, uint16_t* y, EpiExtra ex, void* workspace, hipStream_t st);
+                           int64_t n, int64_t k, uint16_t* y, EpiExtra ex, hipStream_t st);
 
-// The same for few rows (mx4_few.hip), and with the quantizer in the same kernel
-// for the fewest (x BF16 [m, ldx], act as in launch_mx4_quant).
-bool mx4_few_rows(int64_t m, int64_t n, int64_t k);
+// The same for small products (mx4_few.hip; rows of x a workgroup: 16, 32 or 64),
+// and with the quantizer in the same kernel for the fewest rows (x BF16 [m, ldx], act
+// as the quantizer's kind 0 or 1).
 hipError_t launch_mx4_few(const uint8_t* xc, const uint8_t* xs, const uint8_t* wc, const uint8_t* ws, int64_t m, int64_t n,
-                          int64_t k, uint16_t* y, EpiExtra ex, hipStream_t st);
+                          int64_t k, int rows, uint16_t* y, EpiExtra ex, hipStream_t st);
 bool mx4_fused(int64_t m, int64_t k);
 hipError_t launch_mx4_fused(int act, const uint16_t* x, int64_t ldx, const uint8_t* wc, const uint8_t* ws, int64_t m,
                             int64_t n, int64_t k, int g, uint16_t* y, EpiExtra ex, hipStream_t st);

@@ -29,7 +29,6 @@ decltype(&ck_mx4_weight_prep) g_mx4_prep = nullptr;
 decltype(&ck_mx4_act_quant) g_mx4_quant = nullptr;
 decltype(&ck_mx4_dequant) g_mx4_dequant = nullptr;
 decltype(&ck_mx4_gemm_bf16) g_mx4_gemm = nullptr;
-decltype(&ck_mx4_gemm_workspace_size) g_mx4_gemm_size = nullptr;
 decltype(&ck_mx4_linear) g_mx4_linear = nullptr;
 decltype(&ck_mx4_linear_workspace_size) g_mx4_linear_size = nullptr;
 decltype(&ck_block_norm) g_block_norm = nullptr;
@@ -489,16 +488,15 @@ PyObject* mx4_dequant(PyObject*, PyObject* const* a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-// mx4_gemm(x_codes, x_scales, w_codes, w_scales, m, n, bias, residual, out, workspace) -> y, or the C status of a
-// refused call
+// mx4_gemm(x_codes, x_scales, w_codes, w_scales, m, n, bias, residual, out) -> y, or the C status of a refused call
 PyObject* mx4_gemm(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
-    TORCH_CHECK(n == 10 && g_mx4_gemm, "mx4_gemm: 10 arguments, after bind()");
+    TORCH_CHECK(n == 9 && g_mx4_gemm, "mx4_gemm: 9 arguments, after bind()");
     const at::Tensor &xc = tensor_arg(a[0], "activation codes"), &xs = tensor_arg(a[1], "activation scales");
     const at::Tensor &wc = tensor_arg(a[2], "weight codes"), &ws = tensor_arg(a[3], "weight scales");
     const at::Tensor *bias = optional_arg(a[6], "bias"), *residual = optional_arg(a[7], "residual");
-    const at::Tensor *out = optional_arg(a[8], "out"), *work = optional_arg(a[9], "workspace");
+    const at::Tensor* out = optional_arg(a[8], "out");
     TORCH_CHECK_VALUE(xc.is_cuda(), "activation codes must be on a GPU, got ", xc.device());
     const c10::DeviceGuard guard(xc.device());
     check_blocked(xc, xs, "the activation", xc.device());
@@ -511,16 +509,13 @@ PyObject* mx4_gemm(PyObject*, PyObject* const* a, Py_ssize_t n)
     void* stream = stream_of(xc, &failed);
     if (failed) return nullptr;
     Reads reads;
-    if (out || work) reads.add({&xc, &xs, &wc, &ws, bias});
+    if (out) reads.add({&xc, &xs, &wc, &ws, bias});
     const at::Tensor y = linear_out(out, m, nn, xc.options(), reads, bias, residual);
-    if (work) reads.add({residual});
-    const at::Tensor room = room_of(work, g_mx4_gemm_size(m, k, nn), xc.options(), reads, y);
     ck_status st;
     Py_BEGIN_ALLOW_THREADS
     st = g_mx4_gemm((const uint8_t*)xc.data_ptr(), (const uint8_t*)xs.data_ptr(), (const uint8_t*)wc.data_ptr(),
                     (const uint8_t*)ws.data_ptr(), ptr_or_null<const float>(bias),
-                    ptr_or_null<const uint16_t>(residual), m, nn, k, (uint16_t*)y.data_ptr(), ptr(room), bytes(room),
-                    stream);
+                    ptr_or_null<const uint16_t>(residual), m, nn, k, (uint16_t*)y.data_ptr(), stream);
     Py_END_ALLOW_THREADS
     if (st != CK_OK) return PyLong_FromLong(st);
     return THPVariable_Wrap(y);
@@ -713,8 +708,8 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     void** const slots[] = {
         (void**)&g_norm, (void**)&g_attn, (void**)&g_attn_size, (void**)&g_mx4_prep, (void**)&g_mx4_quant,
-        (void**)&g_mx4_dequant, (void**)&g_mx4_gemm, (void**)&g_mx4_gemm_size, (void**)&g_mx4_linear,
-        (void**)&g_mx4_linear_size, (void**)&g_block_norm};
+        (void**)&g_mx4_dequant, (void**)&g_mx4_gemm, (void**)&g_mx4_linear, (void**)&g_mx4_linear_size,
+        (void**)&g_block_norm};
     constexpr int kSlots = sizeof(slots) / sizeof(slots[0]);
     if (n != kSlots + 1) {
         PyErr_Format(PyExc_TypeError, "bind: %d arguments", kSlots + 1);

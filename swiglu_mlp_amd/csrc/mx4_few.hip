@@ -1,14 +1,16 @@
 // mx4_few.hip -- the product of microscaled 4-bit operands (include/ck.h, "MX FP4
-// linears") for few rows of x: the weight streamed once, straight into the matrix
-// cores' registers.
+// linears") where it is small: few rows of x, the weight streamed once, or few
+// tiles.  Both operands go straight into the matrix cores' registers.
 //
 // With few rows nothing but the weight's bytes counts, and the time of a call
-// that moves 25 MB is latency: so a workgroup takes 16 NA rows of the weight and
-// its 8 waves share k, every wave with its first loads on their way before it does
-// anything else.  v_mfma_scale_f32_16x16x128_f8f6f4 takes 16 weight rows (its A
-// operand) and 16 rows of x (B) over 128 values; in the blocked layout a lane's 16
-// bytes of either lie in runs of 256 bytes.  The waves' sums meet in LDS, in a
-// fixed order.
+// that moves 25 MB is latency, as it is with few tiles: so a workgroup takes 16 NA
+// rows of the weight and 16 MF rows of x, and its 8 waves share k, every wave with
+// its first loads on their way before it does anything else.
+// v_mfma_scale_f32_16x16x128_f8f6f4 takes 16 weight rows (its A operand) and 16 rows
+// of x (B) over 128 values; in the blocked layout a lane's 16 bytes of either lie in
+// runs of 256 bytes.  The waves' sums meet in LDS, in a fixed order.  No barrier and
+// no LDS before that: next to the tiles of mx4_gemm.hip a call starts and ends 2 us
+// sooner, but it reads each operand once for every workgroup.
 //
 // FUSED: while the weight's loads are in flight the workgroup quantizes the rows
 // of x itself, into LDS, so the call is one launch; every workgroup repeats that,
@@ -39,6 +41,7 @@ struct FewArgs {
     EpiExtra ex;
     int M, N, k, log_g;
     int pairs;                  // kp / 256
+    int units, m_tiles;         // of 16 NA weight rows, of 16 MF rows of x
     int xb, wb;                 // 32-row blocks
 };
 
@@ -66,9 +69,9 @@ __device__ __forceinline__ uint4 quantize32_by(int log_g, float (&v)[4][8], int 
 }
 
 // NA x MF fragments of 16 x 16 a workgroup.  ACT (FUSED): 0 x, 1 silu(gate) * up.
-// Two workgroups a CU (at most 128 registers), but for 128 rows of x.
+// Two workgroups a CU (at most 128 registers), but for 4 x 4 fragments.
 template <int NA, int MF, bool FUSED, int ACT>
-__global__ __launch_bounds__(kThreads, MF > 4 ? 2 : 4) void mx4_few_kernel(FewArgs g)
+__global__ __launch_bounds__(kThreads, NA * MF > 4 ? 2 : 4) void mx4_few_kernel(FewArgs g)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
     constexpr int UB = (FUSED ? NA : NA + MF) <= 3 ? 2 : 1;   // pairs of a batch
@@ -79,9 +82,12 @@ __global__ __launch_bounds__(kThreads, MF > 4 ? 2 : 4) void mx4_few_kernel(FewAr
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    // neighbouring units (halves of a 32-row block) on one XCD
-    const int G = gridDim.x, b = blockIdx.x;
-    const int unit = (G & 7) == 0 ? (b & 7) * (G >> 3) + (b >> 3) : b;
+    // One XCD (workgroup % 8) takes consecutive tiles, and a unit's lie together, so
+    // that its L2 holds the unit's weight rows.
+    const int each = gridDim.x >> 3, tile = (blockIdx.x & 7) * each + (blockIdx.x >> 3);
+    const int unit = tile / g.m_tiles;
+    if (unit >= g.units) return;
+    const int row0 = (tile - unit * g.m_tiles) * (16 * MF);   // of x
     const int r = lane & 15, kg = lane >> 4;
     const int kb = 4 * g.pairs;
 
@@ -101,7 +107,7 @@ __global__ __launch_bounds__(kThreads, MF > 4 ? 2 : 4) void mx4_few_kernel(FewAr
     if constexpr (!FUSED) {
 #pragma unroll
         for (int j = 0; j < MF; ++j) {
-            const int rb = min(j >> 1, g.xb - 1);
+            const int rb = min((row0 >> 5) + (j >> 1), g.xb - 1);
             xc[j] = g.xc + codes_at(rb, j & 1);
             xs[j] = g.xs + scales_at(rb, j & 1);
         }
@@ -178,9 +184,9 @@ __global__ __launch_bounds__(kThreads, MF > 4 ? 2 : 4) void mx4_few_kernel(FewAr
                     uint32_t s[2];
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        const int at = p * 8 + 4 * t + kg;
-                        const bool ok = r < g.M && at < blocks;
-                        const int place = ok ? r * blocks + at : 0;
+                        const int b = p * 8 + 4 * t + kg;
+                        const bool ok = r < g.M && b < blocks;
+                        const int place = ok ? r * blocks + b : 0;
                         const v4i c = *reinterpret_cast<const v4i*>(smem + place * 16);
                         const uint32_t e = (uint8_t)smem[CODES + place];
                         bx[t][j] = ok ? c : v4i{};
@@ -220,7 +226,7 @@ __global__ __launch_bounds__(kThreads, MF > 4 ? 2 : 4) void mx4_few_kernel(FewAr
     __syncthreads();
     for (int t = tid; t < F * 64; t += kThreads) {
         const int f = t >> 6, l = t & 63;
-        const int m = (f % MF) * 16 + (l & 15), n = (unit * NA + f / MF) * 16 + 4 * (l >> 4);
+        const int m = row0 + (f % MF) * 16 + (l & 15), n = (unit * NA + f / MF) * 16 + 4 * (l >> 4);
         if (m >= g.M || n >= g.N) continue;
         v4f s = *reinterpret_cast<const v4f*>(smem + t * 16);
 #pragma unroll
@@ -233,37 +239,29 @@ __global__ __launch_bounds__(kThreads, MF > 4 ? 2 : 4) void mx4_few_kernel(FewAr
 }
 
 template <int NA, int MF, bool FUSED, int ACT>
-hipError_t launch_few(const FewArgs& g, hipStream_t st)
+hipError_t launch_few(FewArgs g, hipStream_t st)
 {
-    mx4_few_kernel<NA, MF, FUSED, ACT><<<dim3((g.N + 16 * NA - 1) / (16 * NA)), dim3(kThreads), 0, st>>>(g);
+    g.units = (g.N + 16 * NA - 1) / (16 * NA);
+    g.m_tiles = (g.M + 16 * MF - 1) / (16 * MF);
+    const dim3 grid((g.units * g.m_tiles + 7) / 8 * 8);
+    mx4_few_kernel<NA, MF, FUSED, ACT><<<grid, dim3(kThreads), 0, st>>>(g);
     return hipGetLastError();
 }
 
 }  // namespace mx4
 
-// Up to 32 rows always; up to 128 of a narrow weight (one workgroup a CU) and of a k
-// that the waves get through before the tiles' second launch pays, whose operands
-// are shared by more rows.  Measured, this kernel and the tiles: 32 x 2048 -> 24576
-// 6.6 and 8.2 us, 128 x 4096 -> 4096 5.9 and 7.0, 128 x 12288 -> 4096 12.5 and 13.0,
-// 128 x 16384 -> 1024 14.0 and 11.7, 64 x 32768 -> 4096 22.9 and 19.0, 33 x 4096 ->
-// 8176 8.2 and 7.1.
-bool mx4_few_rows(int64_t m, int64_t n, int64_t k)
-{
-    return m <= 32 || (m <= 128 && n <= 16 * num_cus() && m * k <= 3 << 19);
-}
-
+// rows: of x a workgroup, 16, 32 or 64.
 hipError_t launch_mx4_few(const uint8_t* xc, const uint8_t* xs, const uint8_t* wc, const uint8_t* ws, int64_t m, int64_t n,
-                          int64_t k, uint16_t* y, EpiExtra ex, hipStream_t st)
+                          int64_t k, int rows, uint16_t* y, EpiExtra ex, hipStream_t st)
 {
     mx4::FewArgs g{};
     g.xc = xc, g.xs = xs, g.wc = wc, g.ws = ws, g.y = y, g.ex = ex;
     g.M = (int)m, g.N = (int)n, g.k = (int)k, g.pairs = (int)(mx4::pad_cols(k) / 256);
     g.xb = (int)(mx4::pad_rows(m) / 32), g.wb = (int)(mx4::pad_rows(n) / 32);
-    const bool wide = n >= 32 * num_cus();   // 32 rows of the weight a workgroup still give every CU one
-    if (m <= 16) return wide ? mx4::launch_few<2, 1, false, 0>(g, st) : mx4::launch_few<1, 1, false, 0>(g, st);
-    if (m <= 32) return wide ? mx4::launch_few<2, 2, false, 0>(g, st) : mx4::launch_few<1, 2, false, 0>(g, st);
-    if (m <= 64) return mx4::launch_few<1, 4, false, 0>(g, st);
-    return mx4::launch_few<1, 8, false, 0>(g, st);
+    if (rows == 64) return mx4::launch_few<4, 4, false, 0>(g, st);
+    if (rows == 32) return mx4::launch_few<2, 2, false, 0>(g, st);
+    // 32 rows of the weight a workgroup where they still give every CU one
+    return n >= 32 * num_cus() ? mx4::launch_few<2, 1, false, 0>(g, st) : mx4::launch_few<1, 1, false, 0>(g, st);
 }
 
 bool mx4_fused(int64_t m, int64_t k)

@@ -24,14 +24,13 @@
 //    loads are placed between the products in source order.
 //  * Two stages make a pair: 256 values, one chunk of scales (256 bytes for 32
 //    rows; one DMA instruction a wave, one register a fragment).  Slots, scale
-//    selects and the ends of units are constants of a stage's place in its pair.
+//    selects and the ends of tiles are constants of a stage's place in its pair.
 //  * Tiles of 256 columns, one group a CU: workgroups stay and take tiles in turn; the
 //    stages run on from a tile to the next, whose loads so overlap the epilogue.
 //    The workgroups of an XCD take consecutive tiles and share operands in its L2.
 //  * Smaller tiles, two groups a workgroup, each with half of k: their waves fill
 //    each other's gaps, and their sums meet in LDS.
-//  * Few tiles: k is split over several workgroups too, which write FP32 partial
-//    sums that a second kernel adds in a fixed order.
+// Small products take mx4_few.hip instead.
 // Measured: 4096 x 4096 -> 24576 191 us (4.3 PFLOP/s; zeros, whose products cost no
 // power, 131 us), 16384 x 12288 -> 4096 333 us (4.95; zeros 219), with a residual of
 // 134 MB 370.  The matrix cores are busy 55 and 62% of the cycles at 1.8 and 1.7 GHz:
@@ -158,13 +157,12 @@ struct Cfg {
 
 struct Args {
     const uint8_t *xc, *xs, *wc, *ws;
-    void* out;          // BF16 [M, N], or the FP32 partial sums [splits][M][N]
+    uint16_t* y;
     EpiExtra ex;
     int M, N;
     int kb;             // 1 KB blocks (slices) of a 32-row block: kp / 64
     int xb, wb;         // 32-row blocks of x and w
     int tiles_m, tiles_n, group_m;
-    int splits;
 };
 
 // Tile j of the grouped order -> (tm, tn): columns of `group_m` tile-rows.
@@ -178,8 +176,8 @@ __device__ __forceinline__ void tile_coords(int j, int tiles_m, int tiles_n, int
     tn = (j % width) / gm;
 }
 
-// PART: FP32 partial sums out (64 x 64 tiles).  EXTRA: bias and / or residual.
-template <int BM, int BN, int GROUPS, bool PART, bool EXTRA>
+// EXTRA: bias and / or residual.
+template <int BM, int BN, int GROUPS, bool EXTRA>
 __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
 {
     // The body uses AMDGPU-only types; the host pass only needs the launch stub.
@@ -196,7 +194,7 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
     constexpr int H0 = NPAIR / 2;                       // of them, in the first half
     constexpr int L0 = (H0 < C::AP ? H0 : C::AP) * (C::AW > 1 ? 2 : 1) +
                        (H0 > C::AP ? H0 - C::AP : 0) * (C::XW > 1 ? 2 : 1);   // as instructions
-    constexpr int NST = PART ? 0 : 2 * NMF;             // stores of an epilogue (PART: too many to count, waited for)
+    constexpr int NST = 2 * NMF;                        // stores of an epilogue
     // Loads issued after the last of stage s + 1 at the middle of stage s: those of
     // s + 2 .. s + P - 1, the first half's of s + P, and the scales with every second one of these.
     constexpr int OUTS = (C::P - 2) * C::L + L0 + R - 1;
@@ -207,36 +205,33 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
     const int group = GROUPS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) : 0;
     const int G = gridDim.x, b = blockIdx.x;
     const int tiles = g.tiles_m * g.tiles_n;
-    const int units = tiles * g.splits;                 // a tile and one of the splits of k, split-major
-    const int my_units = (units - b + G - 1) / G;       // more than one only with one group and one split
-    const int all_pairs = g.kb / 4, ranges = g.splits * GROUPS;
+    const int my_tiles = (tiles - b + G - 1) / G;       // one with several groups
+    const int all_pairs = g.kb / 4;
 
-    // Within a full round the workgroups of one XCD (b % 8) take consecutive units.
+    // Within a full round the workgroups of one XCD (b % 8) take consecutive tiles.
     const bool xcd_order = (G & 7) == 0;
     const int b_xcd = (b & 7) * (G >> 3) + (b >> 3);
-    auto unit_of = [&](int q) {
-        const bool full = xcd_order & ((q + 1) * G <= units);
+    auto tile_of = [&](int q) {
+        const bool full = xcd_order & ((q + 1) * G <= tiles);
         return q * G + (full ? b_xcd : b);
     };
-    // this group's range of pairs (at least one: there are no more ranges than pairs)
-    const int range = (GROUPS > 1 || PART) ? (unit_of(0) / tiles) * GROUPS + group : 0;
-    const int pair0 = (int)((int64_t)range * all_pairs / ranges);
-    const int pairs = (int)((int64_t)(range + 1) * all_pairs / ranges) - pair0;
-    const int most_pairs = (all_pairs + ranges - 1) / ranges;
+    // this group's range of pairs (of two or more groups at least two pairs each)
+    const int pair0 = group * all_pairs / GROUPS;
+    const int pairs = (group + 1) * all_pairs / GROUPS - pair0;
+    const int most_pairs = (all_pairs + GROUPS - 1) / GROUPS;
     const uint32_t ring = (uint32_t)(uintptr_t)(lds_void_t*)smem + (uint32_t)(group * C::RING);
     const uint32_t lane16 = (uint32_t)lane * 16u;
 
-    // ---- the load cursor: the stage to be loaded next.  After the last unit it
+    // ---- the load cursor: the stage to be loaded next.  After the last tile it
     // starts over on it: those loads go to slots that nobody reads again, and the
     // number of loads of a stage stays constant. ----
     int lq = 0, lpairs = pairs;
     v4i rs_w, rs_x;                                     // the tile's rows of codes
     uint32_t so_w[C::AP], so_x[C::XP];                  // where in them this wave's loads of the stage are
     const uint8_t* sp;                                  // this lane's scales of the pair
-    auto set_unit = [&](int q) {
-        const int u = unit_of(q);
+    auto set_tile = [&](int q) {
         int tm, tn;
-        tile_coords(u % tiles, g.tiles_m, g.tiles_n, g.group_m, tm, tn);
+        tile_coords(tile_of(q), g.tiles_m, g.tiles_n, g.group_m, tm, tn);
         const int64_t wb0 = (int64_t)tn * (BN / 32), xb0 = (int64_t)tm * (BM / 32);
         const int64_t w0 = wb0 * g.kb * 1024, x0 = xb0 * g.kb * 1024;
         // blocks past the operand's end are outside the buffer and read as zero
@@ -282,8 +277,8 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
         if (--lpairs == 0) {
             asm volatile("" ::: "memory");   // a branch, not its ~100 scalar operations in every pair
             lpairs = pairs;
-            lq = min(lq + 1, my_units - 1);
-            set_unit(lq);
+            lq = min(lq + 1, my_tiles - 1);
+            set_tile(lq);
         }
     };
 
@@ -301,7 +296,7 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
         return *reinterpret_cast<const int*>(ps + slot * 4096 + (c / C::CPW) * 1024 + (c % C::CPW) * 256);
     };
 
-    set_unit(0);
+    set_tile(0);
 #pragma unroll
     for (int p = 0; p < C::P; ++p) {
         if (p % 2 == 0) issue_scales(p / 2);
@@ -405,14 +400,13 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
         const int t = (int)threadIdx.x;
         if (t < BN) reinterpret_cast<float*>(smem + SUMS)[t] = g.ex.bias[min(tn * BN + t, g.N - 1)];
     };
-    auto epilogue = [&](int u, int j0, int j1) {
+    auto epilogue = [&](int tile, int j0, int j1) {
         int tm, tn;
-        tile_coords(u % tiles, g.tiles_m, g.tiles_n, g.group_m, tm, tn);
+        tile_coords(tile, g.tiles_m, g.tiles_n, g.group_m, tm, tn);
         const int64_t row0 = (int64_t)tm * BM;
         const int rows = (int)min((int64_t)BM, g.M - row0);
-        constexpr int B = PART ? 4 : 2;
-        char* base = static_cast<char*>(g.out) + ((PART ? (int64_t)(u / tiles) * g.M : 0) + row0) * g.N * B;
-        const __amdgpu_buffer_rsrc_t rs_o = __builtin_amdgcn_make_buffer_rsrc(base, (short)0, rows * g.N * B, 0x00020000);
+        const __amdgpu_buffer_rsrc_t rs_o =
+            __builtin_amdgcn_make_buffer_rsrc(g.y + row0 * g.N, (short)0, rows * g.N * 2, 0x00020000);
         const int n_base = tn * BN + wn0 + 8 * lh;
         // The residual's row j is loaded while row j - 1 is stored; the bias, which
         // every row needs, waits in LDS.
@@ -451,7 +445,7 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
                 for (int h = 0; h < 2; ++h) {
                     const int n = n_base + 32 * i + 16 * h;
                     const bool ok = n < g.N;
-                    if constexpr (!PART && !EXTRA) {
+                    if constexpr (!EXTRA) {
                         const auto r0 = __builtin_amdgcn_permlane32_swap(
                             pack_bf16x2(f[8 * h], f[8 * h + 1]), pack_bf16x2(f[8 * h + 4], f[8 * h + 5]), false, false);
                         const auto r1 = __builtin_amdgcn_permlane32_swap(
@@ -467,27 +461,19 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
                             v[e] = __uint_as_float(t[0]);
                             v[4 + e] = __uint_as_float(t[1]);
                         }
-                        if constexpr (PART) {
-                            const uint32_t o = ok ? (row + (uint32_t)n) * 4u : kBufferOutside;
-                            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, v4f{v[0], v[1], v[2], v[3]}), rs_o,
-                                                                   r < rows ? o : kBufferOutside, 0, 0);
-                            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, v4f{v[4], v[5], v[6], v[7]}), rs_o,
-                                                                   r < rows && ok ? o + 16u : kBufferOutside, 0, 0);
-                        } else {
-                            if (g.ex.bias) {
-                                const float* lb = reinterpret_cast<const float*>(smem + SUMS) + wn0 + 8 * lh + 32 * i + 16 * h;
+                        if (g.ex.bias) {
+                            const float* lb = reinterpret_cast<const float*>(smem + SUMS) + wn0 + 8 * lh + 32 * i + 16 * h;
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) v[e] = v[e] + lb[e];
-                            }
-                            if (g.ex.res) {
-                                float x[8];
-                                unpack8<bf16>(res[j & 1][2 * i + h], x);
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) v[e] = v[e] + x[e];
-                            }
-                            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, pack8<bf16>(v)), rs_o,
-                                                                   ok ? (row + (uint32_t)n) * 2u : kBufferOutside, 0, 0);
+                            for (int e = 0; e < 8; ++e) v[e] = v[e] + lb[e];
                         }
+                        if (g.ex.res) {
+                            float x[8];
+                            unpack8<bf16>(res[j & 1][2 * i + h], x);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) v[e] = v[e] + x[e];
+                        }
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, pack8<bf16>(v)), rs_o,
+                                                               ok ? (row + (uint32_t)n) * 2u : kBufferOutside, 0, 0);
                     }
                 }
                 __builtin_amdgcn_sched_barrier(0);
@@ -502,29 +488,24 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
     constexpr std::true_type first{};
     constexpr std::false_type later{};
     if constexpr (GROUPS == 1) {
-        for (int q = 0; q < my_units; ++q) {
+        for (int q = 0; q < my_tiles; ++q) {
             stage(first, even, more, q > 0);
             stage(later, odd, more, q > 0);
             for (int p = 1; p < pairs; ++p) {
                 stage(later, even, more, false);
                 stage(later, odd, more, false);
             }
-            epilogue(unit_of(q), 0, C::FM);
+            epilogue(tile_of(q), 0, C::FM);
         }
         wait_vmcnt<0>();   // no LDS load may land after the workgroup retires
     } else {
-        // (of one pair only the prologue's third stage is loaded for nothing)
-        if (pairs == 1) {
-            stage(first, even, one_left, false);
-        } else {
-            stage(first, even, more, false);
-            for (int p = 2; p < pairs; ++p) {
-                stage(later, odd, more, false);
-                stage(later, even, more, false);
-            }
-            stage(later, odd, two_left, false);
-            stage(later, even, one_left, false);
+        stage(first, even, more, false);
+        for (int p = 2; p < pairs; ++p) {
+            stage(later, odd, more, false);
+            stage(later, even, more, false);
         }
+        stage(later, odd, two_left, false);
+        stage(later, even, one_left, false);
         stage(later, odd, last, false);
         if (pairs < most_pairs) {   // as many barriers in every group
             workgroup_barrier();
@@ -552,7 +533,7 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
         }
         if (EXTRA && g.ex.bias) {
             int tm, tn;
-            tile_coords(unit_of(0) % tiles, g.tiles_m, g.tiles_n, g.group_m, tm, tn);
+            tile_coords(tile_of(0), g.tiles_m, g.tiles_n, g.group_m, tm, tn);
             stage_bias(tn);
         }
         __syncthreads();
@@ -573,36 +554,9 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
                     }
             }
         }
-        epilogue(unit_of(0), group * SHARE, (group + 1) * SHARE);
+        epilogue(tile_of(0), group * SHARE, (group + 1) * SHARE);
     }
 #endif  // __HIP_DEVICE_COMPILE__
-}
-
-// y from `splits` FP32 partial sums [splits][M][N], added in order; 8 outputs a thread.
-__global__ __launch_bounds__(256) void mx4_join_kernel(const float* __restrict__ part, int splits, int64_t M, int N,
-                                                       EpiExtra ex, uint16_t* __restrict__ y)
-{
-    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
-    if (at >= M * N) return;
-    float v[8] = {};
-    for (int s = 0; s < splits; ++s) {
-        const float4* p = reinterpret_cast<const float4*>(part + s * M * N + at);
-        const float4 a = p[0], b = p[1];
-        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-        v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
-    }
-    if (ex.bias) {
-        const int n = (int)(at % N);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = v[e] + ex.bias[n + e];
-    }
-    if (ex.res) {
-        float r[8];
-        unpack8<bf16>(*reinterpret_cast<const uint4*>(ex.res + at), r);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = v[e] + r[e];
-    }
-    *reinterpret_cast<uint4*>(y + at) = pack8<bf16>(v);
 }
 
 template <int BM, int BN, int GROUPS>
@@ -612,98 +566,63 @@ hipError_t launch(Args g, int num_cu, hipStream_t st)
     g.tiles_m = (g.M + BM - 1) / BM;
     g.tiles_n = (g.N + BN - 1) / BN;
     g.group_m = std::min(g.tiles_m, 4);
-    const int units = g.tiles_m * g.tiles_n * g.splits;
-    const dim3 grid(GROUPS > 1 ? units : std::min(units, num_cu)), block(256 * GROUPS);
-    if (BM == 64 && BN == 64 && g.splits > 1)
-        mx4_gemm_kernel<64, 64, 2, true, false><<<grid, block, 0, st>>>(g);
-    else if (extra)
-        mx4_gemm_kernel<BM, BN, GROUPS, false, true><<<grid, block, 0, st>>>(g);
+    const int tiles = g.tiles_m * g.tiles_n;
+    const dim3 grid(GROUPS > 1 ? tiles : std::min(tiles, num_cu)), block(256 * GROUPS);
+    if (extra)
+        mx4_gemm_kernel<BM, BN, GROUPS, true><<<grid, block, 0, st>>>(g);
     else
-        mx4_gemm_kernel<BM, BN, GROUPS, false, false><<<grid, block, 0, st>>>(g);
+        mx4_gemm_kernel<BM, BN, GROUPS, false><<<grid, block, 0, st>>>(g);
     return hipGetLastError();
 }
 
-// How a product runs: which tiles, over how many splits of k.
-struct Plan {
-    int bm, bn, splits;
-};
-
-// Tiles and what a call on them takes in us: start + rounds (unit + pair pairs), a
-// round being a tile a CU and a pair 256 of k.  Measured: 4096 x 4096 -> 24576, 6
-// rounds of 256 x 256 tiles, 198 us (128 x 256: 226); 2048 x 4096 -> 4096 22 us on
-// 128 x 256 (128 x 128: 28, 256 x 256 on half of the CUs: 28); 1024 x 4096 -> 4096
-// 14 us on 128 x 128 (64 x 128: 19, 128 x 256: 17); 512 x 4096 -> 4096 10.2 us on 64
-// x 128 (128 x 128: 11.5, 64 x 64: 12.2); 256 x 4096 -> 4096 7.7 us on 64 x 64 (64 x
-// 128: 8.9), with k = 12288 14.5.
+// Tiles, and what a call on them takes in us: start + rounds (unit + pair pairs), a
+// round being a tile a CU and a pair 256 of k.  The last two are mx4_few.hip's.
+// Measured: 4096 x 4096 -> 24576, 6 rounds of 256 x 256 tiles, 198 us (128 x 256:
+// 226); 2048 x 4096 -> 4096 22 us on 128 x 256 (128 x 128: 28, 256 x 256 on half of
+// the CUs: 28); 1024 x 4096 -> 4096 14 us on 128 x 128 (64 x 128: 19, 128 x 256: 17);
+// 512 x 4096 -> 4096 10.0 us on 64 x 128 (128 x 128: 11.5, 64 x 64: 12.0); 256 x 4096
+// -> 4096 6.8 us on 64 x 64 (32 x 32: 8.6, 64 x 128: 8.9), with k = 12288 13.3 (64 x
+// 128: 17); 333 x 2112 -> 1040 4.4 us on 32 x 32 (64 x 64: 5.0, 64 x 128: 6.8).
 struct Shape {
     int bm, bn, groups;
     float start, unit, pair;
 };
-constexpr Shape kShapes[] = {{256, 256, 1, 3.0f, 9.0f, 1.5f},
-                             {128, 256, 1, 4.0f, 4.0f, 0.93f},
-                             {128, 128, 2, 2.5f, 4.0f, 0.5f},
-                             {64, 128, 2, 1.5f, 3.4f, 0.33f},
-                             {64, 64, 2, 2.3f, 2.0f, 0.21f}};
+constexpr Shape kShapes[] = {{256, 256, 1, 3.0f, 9.0f, 1.5f}, {128, 256, 1, 4.0f, 4.0f, 0.93f},
+                             {128, 128, 2, 2.5f, 4.0f, 0.5f}, {64, 128, 2, 1.5f, 3.4f, 0.33f},
+                             {64, 64, 1, 2.6f, 0.6f, 0.222f}, {32, 32, 1, 2.6f, 0.3f, 0.079f}};
 
-Plan plan_of(int64_t m, int64_t n, int64_t k, int num_cu)
+const Shape& shape_of(int64_t m, int64_t n, int64_t k, int num_cu)
 {
     const int64_t pairs = pad_cols(k) / 256;
-    Plan best{};
+    const Shape* best = nullptr;
     double least = 0;
     for (const Shape& c : kShapes) {
-        if (pairs < c.groups) continue;
+        if (c.groups > 1 && pairs < 2 * c.groups) continue;   // two pairs a group
         const int64_t tiles = ((m + c.bm - 1) / c.bm) * ((n + c.bn - 1) / c.bn), rounds = (tiles + num_cu - 1) / num_cu;
+        // a workgroup a tile: kept to half of a launch's 2^32 threads
+        if (c.bn < 256 && tiles > 1 << 22) continue;
         const double t = c.start + (double)rounds * (c.unit + c.pair * (double)pairs);
-        if (least == 0 || t < least) best = {c.bm, c.bn, 1}, least = t;
+        if (!best || t < least) best = &c, least = t;
     }
-    // Few of the smallest tiles and a long k: the splits' partial sums cost a second
-    // launch and their way through memory, 4 to 5 us (128 x 12288 -> 4096: 13 us, in
-    // two splits 16; 129 x 32768 -> 256: 27 us, in eight 12; 256 x 12288 -> 256: 12.4
-    // and 10.7).
-    if (best.bm == 64 && best.bn == 64) {
-        const int64_t tiles = ((m + 63) / 64) * ((n + 63) / 64);
-        int s = 1;
-        while (tiles * s * 2 <= num_cu && s < 8 && pairs / (s * 2) >= 8) s *= 2;
-        if (0.21 * (double)pairs * (1.0 - 1.0 / s) > 6.5) best.splits = s;
-    }
-    return best;
+    return *best;
 }
 
 }  // namespace mx4
 
-size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k)
-{
-    if (mx4_few_rows(m, n, k)) return 0;
-    const mx4::Plan p = mx4::plan_of(m, n, k, num_cus());
-    return p.splits > 1 ? (size_t)p.splits * (size_t)m * (size_t)n * 4 : 0;
-}
-
 hipError_t launch_mx4_gemm(const uint8_t* xc, const uint8_t* xs, const uint8_t* wc, const uint8_t* ws, int64_t m,
-                           int64_t n, int64_t k, uint16_t* y, EpiExtra ex, void* workspace, hipStream_t st)
+                           int64_t n, int64_t k, uint16_t* y, EpiExtra ex, hipStream_t st)
 {
-    if (mx4_few_rows(m, n, k)) return launch_mx4_few(xc, xs, wc, ws, m, n, k, y, ex, st);
+    if (m <= 16) return launch_mx4_few(xc, xs, wc, ws, m, n, k, 16, y, ex, st);
     const int num_cu = num_cus();
-    const mx4::Plan p = mx4::plan_of(m, n, k, num_cu);
+    const mx4::Shape& c = mx4::shape_of(m, n, k, num_cu);
+    if (c.bn <= 64) return launch_mx4_few(xc, xs, wc, ws, m, n, k, c.bm, y, ex, st);
     mx4::Args g{};
-    g.xc = xc, g.xs = xs, g.wc = wc, g.ws = ws;
+    g.xc = xc, g.xs = xs, g.wc = wc, g.ws = ws, g.y = y, g.ex = ex;
     g.M = (int)m, g.N = (int)n, g.kb = (int)(mx4::pad_cols(k) / 64);
     g.xb = (int)(mx4::pad_rows(m) / 32), g.wb = (int)(mx4::pad_rows(n) / 32);
-    g.splits = p.splits;
-    g.out = p.splits > 1 ? workspace : y;
-    if (p.splits == 1) g.ex = ex;
-    hipError_t e = hipErrorNotSupported;
-    switch (p.bm * 1000 + p.bn) {
-        case 256256: e = mx4::launch<256, 256, 1>(g, num_cu, st); break;
-        case 128256: e = mx4::launch<128, 256, 1>(g, num_cu, st); break;
-        case 128128: e = mx4::launch<128, 128, 2>(g, num_cu, st); break;
-        case 64128: e = mx4::launch<64, 128, 2>(g, num_cu, st); break;
-        default: e = mx4::launch<64, 64, 2>(g, num_cu, st); break;
-    }
-    if (e != hipSuccess || p.splits == 1) return e;
-    const int64_t threads = m * n / 8;
-    mx4::mx4_join_kernel<<<dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, st>>>(
-        static_cast<const float*>(workspace), p.splits, m, (int)n, ex, y);
-    return hipGetLastError();
+    if (c.bm == 256) return mx4::launch<256, 256, 1>(g, num_cu, st);
+    if (c.bn == 256) return mx4::launch<128, 256, 1>(g, num_cu, st);
+    return c.bm == 128 ? mx4::launch<128, 128, 2>(g, num_cu, st) : mx4::launch<64, 128, 2>(g, num_cu, st);
 }
 
 }  // namespace ck

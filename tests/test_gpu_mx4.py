@@ -12,10 +12,9 @@ Bounds elsewhere, u = 2^-8 the largest relative error of a rounding to BF16:
                   another |g| 2^-24 |a|: under 2^-21 |a| in all down to g = -4, and below
                   that |a| < |u| / 13 falls faster than |g| grows.  A code is then the
                   nearest of values within t, and a scale that of such a maximum.
-  product         every one of the k products is exact in FP32 and passes at most 64
-                  roundings in its instruction and one in each of the k / 64
-                  that follow, and as many again as there are splits of k (under
-                  64), all of partial sums within A = sum |x w|:
+  product         every one of the k products is exact in FP32 and passes at most 128
+                  roundings in its instruction and one in each of the at most
+                  k / 64 sums that follow, of partial sums within A = sum |x w|:
                   (128 + k / 64) 2^-23 A (2^-23: the matrix cores may truncate),
                   the bias' and the residual's sums 2^-24 of their terms, and u |y|.
 """
@@ -240,13 +239,14 @@ def check_product(y, xv, wv, bias=None, residual=None, what=""):
     assert (off <= bound * (1 + 2.0 ** -8) + 1e-38).all(), (what, (off / (bound + 1e-38)).max().item())
 
 
-# every kernel and tile, one or more tiles a workgroup, even and odd shares of k, splits of k
+# every kernel and tile, one or more tiles a workgroup, even and odd shares of k
 SIZES = [(1, 16, 64), (1, 12288, 4096), (2, 48, 128), (3, 4096, 12288), (8, 1040, 2112), (15, 80, 320), (16, 4096, 4096),
          (17, 512, 1024), (31, 272, 192), (32, 2048, 12288), (33, 96, 512), (48, 4096, 8192), (63, 1040, 256),
          (64, 64, 32768), (65, 144, 448), (96, 12288, 1024), (128, 128, 12288), (129, 528, 2112), (200, 1024, 8192),
          (256, 256, 256), (257, 272, 64), (333, 1040, 2112), (512, 4096, 512), (1000, 240, 12288), (1024, 1024, 1024),
          (1025, 2064, 576), (2048, 4096, 320), (4096, 4096, 256), (5000, 2992, 448),
-         (20, 8208, 512), (6000, 6000, 2112), (6200, 10000, 2304), (9000, 8000, 320), (2500, 2000, 4160)]
+         (20, 8208, 512), (6000, 6000, 2112), (6200, 10000, 2304), (9000, 8000, 320), (2500, 2000, 4160),
+         (450, 4080, 2816), (500, 4096, 4416), (1000, 4080, 2368), (980, 4096, 1600), (97, 176, 1088), (250, 4000, 4160)]
 
 
 @pytest.mark.parametrize("m,n,k", SIZES)
