@@ -31,9 +31,9 @@
 //  * Smaller tiles, two groups a workgroup, each with half of k: their waves fill
 //    each other's gaps, and their sums meet in LDS.
 // Small products take mx4_few.hip instead.
-// Measured: 4096 x 4096 -> 24576 191 us (4.3 PFLOP/s; zeros, whose products cost no
-// power, 131 us), 16384 x 12288 -> 4096 333 us (4.95; zeros 219), with a residual of
-// 134 MB 370.  The matrix cores are busy 55 and 62% of the cycles at 1.8 and 1.7 GHz:
+// Measured, cards differing by 4%: 4096 x 4096 -> 24576 191 us (4.3 PFLOP/s; zeros,
+// whose products cost no power, 131 us), 16384 x 12288 -> 4096 333 us (4.95; zeros
+// 219), with a residual of 134 MB 370.  The matrix cores are busy 55 and 62% of the cycles at 1.8 and 1.7 GHz:
 // the power is the limit, and what is not a product there costs energy, not time.
 #include "ck_internal.hpp"
 #include "mx4.hpp"
