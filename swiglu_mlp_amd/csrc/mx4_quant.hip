@@ -7,27 +7,38 @@
 // and only the rotation's strides from 32 up cross lanes, within the eight lanes
 // of 256 values.  A wave takes 8 rows x 256 values and a workgroup 32 x 256: in
 // the blocked layout that is 4 KB of codes and 256 bytes of scales, both
-// contiguous, written in pieces of 128 bytes or more.  A lane's four 16-byte loads
-// of a row meet in the same cache lines; marked nontemporal they fetch each line
-// four times (281 us for 176).
+// contiguous, written in pieces of 128 bytes or more.  With SwiGLU, whose rows are
+// two streams, it is 4 x 512 and 16 x 512: reads of 1 KB keep memory busier there
+// (200 million values in rows of 5120, 8192, 12288 and 28672: 170, 155, 161 and 162 us
+// for 187, 157, 172 and 174; rows of 11008 are the other way, 171 for 160), not in one
+// stream (98304 x 4096 171 us for 162).  A lane's four 16-byte loads of a row meet in
+// the same cache lines; marked nontemporal they fetch each line four times (281 us for
+// 176).
 //
-// Bound by HBM: 65536 x 4096 BF16 rotated by 128, 680 MB, 108 us (6.3 TB/s); 16384 x
-// 12288 with SwiGLU, 912 MB, 176 us (5.2); FP32 12288 x 4096, 228 MB, 46 us (5.0);
-// back to BF16, 127 MB, 19.5 us (6.5); 16 rows 2.2 to 4 us, a launch.
+// Bound by HBM: 49152 x 4096 BF16 rotated by 128, 510 MB, 80 us (6.4 TB/s); 16384 x
+// 12288 with SwiGLU, 912 MB, 163 us (5.6; without its arithmetic 8 us less); FP32
+// 12288 x 4096, 228 MB, 46 us (5.0); back to BF16, 127 MB, 19.5 us (6.5); 16 rows
+// 2.2 to 4 us, a launch.
 #include "ck_internal.hpp"
 #include "mx4.hpp"
 
 namespace ck {
 namespace mx4 {
 
+template <int KIND>
+constexpr uint32_t kQuantRows = KIND == 1 ? 16 : 32;   // of a workgroup
+
+// units: of 256 values of a row; wide: workgroups along a row.
 template <int KIND, int LOG_G, bool BLOCKED>
 __global__ __launch_bounds__(256) void mx4_quant_kernel(const void* __restrict__ src, int64_t ld, int64_t m, int64_t k,
-                                                        uint32_t units, uint8_t* __restrict__ codes,
+                                                        uint32_t units, uint32_t wide, uint8_t* __restrict__ codes,
                                                         uint8_t* __restrict__ scales)
 {
-    const uint32_t rb = blockIdx.x / units, unit = blockIdx.x - rb * units;   // 32-row block, 256 values
+    constexpr uint32_t ROWS = kQuantRows<KIND>, LANES = 256 / ROWS;   // lanes of a row
+    const uint32_t rg = blockIdx.x / wide;
+    const uint32_t unit = (blockIdx.x - rg * wide) * (LANES / 8) + threadIdx.x % LANES / 8;
     const int lane = threadIdx.x & 63;
-    const int64_t row = (int64_t)rb * 32 + (threadIdx.x >> 3);
+    const int64_t row = (int64_t)rg * ROWS + threadIdx.x / LANES;
     const uint32_t kb = unit * 8 + (lane & 7);   // the row's block of 32
     const bool live = row < m && (int64_t)kb * 32 < k;
     float v[4][8];
@@ -44,9 +55,9 @@ __global__ __launch_bounds__(256) void mx4_quant_kernel(const void* __restrict__
         // the four scales of a (row, half) in its first lane: lanes + 2, + 4, + 6
         uint32_t w = byte | (uint32_t)__builtin_amdgcn_update_dpp(0, (int)byte, 0x4E, 0xf, 0xf, false) << 8;
         w |= (uint32_t)__builtin_amdgcn_ds_swizzle((int)w, (4 << 10) | 0x1f) << 16;
-        if (row >= m) return;   // padding rows are not written, padding columns are
-        const uint32_t r = threadIdx.x >> 3, h = lane & 1, j = (lane >> 1) & 3;
-        const int64_t chunk = (int64_t)rb * units + unit;
+        if (row >= m || unit >= units) return;   // padding rows are not written, padding columns are
+        const uint32_t r = (uint32_t)row & 31, h = lane & 1, j = (lane >> 1) & 3;
+        const int64_t chunk = (row >> 5) * units + unit;
         *reinterpret_cast<uint4*>(codes + chunk * 4096 + j * 1024 + h * 512 + r * 16) = q;
         if (j == 0) *reinterpret_cast<uint32_t*>(scales + chunk * 256 + (h * 32 + r) * 4) = w;
     } else if (live) {
@@ -119,11 +130,13 @@ hipError_t launch_quant(const void* src, int64_t ld, int64_t m, int64_t k, bool 
                         uint8_t* scales, hipStream_t st)
 {
     const uint32_t units = (uint32_t)(mx4::pad_cols(k) / 256);
-    const dim3 grid((uint32_t)(mx4::pad_rows(m) / 32) * units);
+    constexpr uint32_t rows = mx4::kQuantRows<KIND>, row_units = 32 / rows;
+    const uint32_t wide = (units + row_units - 1) / row_units;
+    const dim3 grid((uint32_t)((m + rows - 1) / rows) * wide);
     if (blocked)
-        mx4::mx4_quant_kernel<KIND, LOG_G, true><<<grid, dim3(256), 0, st>>>(src, ld, m, k, units, codes, scales);
+        mx4::mx4_quant_kernel<KIND, LOG_G, true><<<grid, dim3(256), 0, st>>>(src, ld, m, k, units, wide, codes, scales);
     else
-        mx4::mx4_quant_kernel<KIND, LOG_G, false><<<grid, dim3(256), 0, st>>>(src, ld, m, k, units, codes, scales);
+        mx4::mx4_quant_kernel<KIND, LOG_G, false><<<grid, dim3(256), 0, st>>>(src, ld, m, k, units, wide, codes, scales);
     return hipGetLastError();
 }
 
