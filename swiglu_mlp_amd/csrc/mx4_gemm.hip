@@ -37,6 +37,7 @@
 // the power is the limit, and what is not a product there costs energy, not time.
 #include "ck_internal.hpp"
 #include "mx4.hpp"
+#include "mx4_stage.hpp"
 
 #include <algorithm>
 #include <type_traits>
@@ -232,23 +233,19 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
     auto set_tile = [&](int q) {
         int tm, tn;
         tile_coords(tile_of(q), g.tiles_m, g.tiles_n, g.group_m, tm, tn);
+        // quotients are computed in lanes; what follows from them here are scalar operands
+        tm = __builtin_amdgcn_readfirstlane(tm), tn = __builtin_amdgcn_readfirstlane(tn);
         const int64_t wb0 = (int64_t)tn * (BN / 32), xb0 = (int64_t)tm * (BM / 32);
         const int64_t w0 = wb0 * g.kb * 1024, x0 = xb0 * g.kb * 1024;
-        // blocks past the operand's end are outside the buffer and read as zero
         rs_w = make_rsrc(g.wc + w0, (int64_t)g.wb * g.kb * 1024 - w0);
         rs_x = make_rsrc(g.xc + x0, (int64_t)g.xb * g.kb * 1024 - x0);
-        // block ai of a stage: row block ai / 2, slice ai % 2
 #pragma unroll
-        for (int p = 0; p < C::AP; ++p) {
-            const int ai = wave * C::AW + 2 * p;
-            so_w[p] = (uint32_t)((ai / 2) * g.kb + ai % 2 + pair0 * 4) * 1024u;
-        }
+        for (int p = 0; p < C::AP; ++p)
+            so_w[p] = stage_offset(wave * C::AW + 2 * p, g.kb, pair0 * 4, g.wb - (int)wb0);
 #pragma unroll
-        for (int p = 0; p < C::XP; ++p) {
-            const int ai = wave * C::XW + 2 * p;
-            so_x[p] = (uint32_t)((ai / 2) * g.kb + ai % 2 + pair0 * 4) * 1024u;
-        }
-        // a chunk past the end takes the last block's scales (for products that are not stored)
+        for (int p = 0; p < C::XP; ++p)
+            so_x[p] = stage_offset(wave * C::XW + 2 * p, g.kb, pair0 * 4, g.xb - (int)xb0);
+        // past the operand's end the last block's scales, as with its codes
         const int c = min(wave * C::CPW + min(lane >> 4, C::CPW - 1), C::CHUNKS - 1);
         const bool w = c < BN / 32;
         const int64_t rb = w ? min((int64_t)g.wb - 1, wb0 + c) : min((int64_t)g.xb - 1, xb0 + c - BN / 32);

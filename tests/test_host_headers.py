@@ -159,3 +159,25 @@ def test_views_without_an_element_twice(tmp_path):
         st = [rng.choice([1, 2, 3, 4, 6, 8, 12, 16, 24]) for _ in range(4)]
         if distinct(n, st, size):
             assert len(elements((0, size, n, st))) == size * n[0] * n[1] * n[2] * n[3], (n, st, size)
+
+
+def test_stages_of_the_4_bit_product_read_inside_the_operand(tmp_path):
+    # operands are padded to 32 rows and tiles are up to 256: a tile at the end has row blocks that the operand lacks.
+    # What is read for them is never stored, so only the addresses can show a read behind the operand.
+    L = compiled(tmp_path, "mx4_stage.hpp", 'extern "C" uint32_t at(int block, int kb, int slice0, int left)'
+                                            " { return ck::mx4::stage_offset(block, kb, slice0, left); }")
+    L.at.restype = ctypes.c_uint32
+    for side in (64, 128, 256):                    # rows of a tile: side / 16 blocks of 1 KB a stage
+        for left in list(range(1, side // 32 + 2)) + [1000]:
+            for kb in (4, 8, 12, 20, 128, 512):
+                pairs = kb // 4
+                for groups in (1, 2):              # a group's first pair of stages, and how many
+                    for g in range(groups):
+                        first = g * pairs // groups
+                        stages = 2 * ((g + 1) * pairs // groups - first)
+                        for block in range(side // 16):
+                            at = L.at(block, kb, 4 * first, left)
+                            last = at + max(stages - 1, 0) * 2048 + 1024
+                            assert last <= left * kb * 1024, (side, left, kb, groups, g, block)
+                            if block // 2 < left:
+                                assert at == ((block // 2) * kb + block % 2 + 4 * first) * 1024
