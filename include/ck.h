@@ -451,8 +451,9 @@ size_t ck_cross_attn_workspace_size(int64_t batch, int64_t kv_batch, int64_t tq,
  * byte ((k % 64) / 32) * 512 + (r % 32) * 16 + (k % 32) / 2.  Scales, rp * kp / 32
  * bytes: 256 bytes (r / 32, k / 256) at ((r / 32) * (kp / 256) + k / 256) * 256,
  * inside them the byte (32 ((k % 64) / 32) + r % 32) * 4 + (k % 256) / 64.
- * Padding columns hold zero products; padding rows are never read into valid
- * outputs (an activation's are not written).
+ * Padding rows and columns are zero, codes and scales, in all that the quantizers
+ * and the relayout write.  Of the padding rows, no code or scale reaches a valid row
+ * or column of an output; padding columns must hold zero codes and no scale of 255.
  * Shapes as in the INT8 calls (k % 64 == 0, k % group == 0, n % 16 == 0,
  * k <= CK_MAX_K), with rp * kp < 2^34 for either operand, n < 2^21 and
  * m n < 2^35. */

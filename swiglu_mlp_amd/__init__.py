@@ -767,8 +767,8 @@ def ck_cross_attn(q, k, v, scale=None, kv_len=None, key_mask=None, out=None, wor
 def ck_mx4_weight_prep(w, group: int = 128, layout="blocked"):
     """Rotate and quantize an FP32 weight [n, k] -> (codes, scales), uint8.
     layout "blocked" (default, what the linear reads): codes [n / 32, k / 64,
-    1024] and scales [n / 32, k / 256, 256], n padded to 32 and k to 256;
-    "rows" (serialized): codes [n, k / 2], the even k in the low nibble, and
+    1024] and scales [n / 32, k / 256, 256], n padded to 32 and k to 256 with
+    zeros; "rows" (serialized): codes [n, k / 2], the even k in the low nibble, and
     scales [n, k / 32].  group 1: no rotation."""
     return _done("ck_mx4_weight_prep", (_calls or _native()).mx4_quant(w, CK_ACT_NONE, group, None, _layout_code(layout),
                                                                       True))
@@ -805,14 +805,16 @@ def ck_mx4_act_quant(x, input_act=None, group: int = 128, k: int | None = None, 
 
 def ck_mx4_dequant(codes, scales, rows: int | None = None, k: int | None = None):
     """The values that codes and scales stand for, BF16 [rows, k] (exact).
-    rows and k: the logical sizes of blocked operands (default: with padding)."""
+    rows and k: the logical sizes of blocked operands (default: with the padding,
+    zeros)."""
     return _done("ck_mx4_dequant", (_calls or _native()).mx4_dequant(codes, scales, rows, k))
 
 
 def ck_mx4_gemm_bf16(x_codes, x_scales, w_codes, w_scales, m: int, n: int | None = None, out=None, bias=None,
                      residual=None):
     """y = bf16(x w^T (+ bias) (+ residual)) of blocked 4-bit operands with m and
-    n logical rows (n default: the weight's padded rows)."""
+    n logical rows (n default: the weight's padded rows, whose features are zero
+    before bias and residual)."""
     return _done("ck_mx4_gemm_bf16", (_calls or _native()).mx4_gemm(x_codes, x_scales, w_codes, w_scales, m, n, bias,
                                                                    residual, out))
 
@@ -824,7 +826,8 @@ def ck_mx4_linear(x, w_codes, w_scales, n: int | None = None, group: int = 128, 
     bias [n] and the BF16 residual [m, n].
 
     (w_codes, w_scales) from ck_mx4_weight_prep or ck_mx4_weight_pack, rotated by
-    the same group; n: its out_features when not a multiple of 32.  `out` may be
+    the same group; n: its out_features when not a multiple of 32 (default: with
+    the padding, features that are zero before bias and residual).  `out` may be
     the residual itself and shares no memory with anything else; nor does
     `workspace` (uint8, 256-byte aligned, ck_mx4_linear_workspace_size(m, k, n)
     bytes)."""

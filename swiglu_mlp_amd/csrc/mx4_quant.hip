@@ -50,12 +50,13 @@ __global__ __launch_bounds__(256) void mx4_quant_kernel(const void* __restrict__
     // reaches past k (it divides it)
     if (live) load32<KIND>(src, row * ld + (int64_t)kb * 32, k, v);
     uint32_t byte;
-    const uint4 q = quantize32<LOG_G>(v, lane, &byte);
+    uint4 q = quantize32<LOG_G>(v, lane, &byte);
     if constexpr (BLOCKED) {
         // the four scales of a (row, half) in its first lane: lanes + 2, + 4, + 6
         uint32_t w = byte | (uint32_t)__builtin_amdgcn_update_dpp(0, (int)byte, 0x4E, 0xf, 0xf, false) << 8;
         w |= (uint32_t)__builtin_amdgcn_ds_swizzle((int)w, (4 << 10) | 0x1f) << 16;
-        if (row >= m || unit >= units) return;   // padding rows are not written, padding columns are
+        if (unit >= units) return;   // (the grid ends with the padding rows)
+        if (!live) q = make_uint4(0, 0, 0, 0);   // padding is zero, and so is its scale byte; not the rotation's -0
         const uint32_t r = (uint32_t)row & 31, h = lane & 1, j = (lane >> 1) & 3;
         const int64_t chunk = (row >> 5) * units + unit;
         *reinterpret_cast<uint4*>(codes + chunk * 4096 + j * 1024 + h * 512 + r * 16) = q;
@@ -132,7 +133,8 @@ hipError_t launch_quant(const void* src, int64_t ld, int64_t m, int64_t k, bool 
     const uint32_t units = (uint32_t)(mx4::pad_cols(k) / 256);
     constexpr uint32_t rows = mx4::kQuantRows<KIND>, row_units = 32 / rows;
     const uint32_t wide = (units + row_units - 1) / row_units;
-    const dim3 grid((uint32_t)((m + rows - 1) / rows) * wide);
+    const int64_t all = blocked ? mx4::pad_rows(m) : m;
+    const dim3 grid((uint32_t)((all + rows - 1) / rows) * wide);
     if (blocked)
         mx4::mx4_quant_kernel<KIND, LOG_G, true><<<grid, dim3(256), 0, st>>>(src, ld, m, k, units, wide, codes, scales);
     else

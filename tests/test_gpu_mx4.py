@@ -473,3 +473,44 @@ def test_refusals_of_shared_memory():
                 {"workspace": buf[1 << 17:(1 << 17) + need]}):
         with pytest.raises(ValueError):
             ck.ck_mx4_linear(x, wc, ws, **{**kw, **bad})
+
+
+# ---------------------------------------------------------------- padding
+def fill_free_memory(byte):
+    """What the allocator hands out next holds `byte`."""
+    del [torch.full((1 << i,), byte, dtype=torch.uint8, device=DEV) for i in range(9, 25) for _ in range(4)][:]
+
+
+@pytest.mark.parametrize("n,k,group", [(16, 64, 1), (48, 320, 64), (48, 256, 256), (80, 4096, 128), (272, 576, 2)])
+def test_weight_padding_is_zero(n, k, group):
+    """Quantized here or packed, a weight is the same bytes, and the features that it pads to are zero."""
+    w = torch.randn(n, k, generator=gen(n), device=DEV)
+    rows = ck.ck_mx4_weight_prep(w, group, layout="rows")
+    x = activation(40, k, 5)
+    want = ck.ck_mx4_linear(x, *ck.ck_mx4_weight_pack(*rows), n=n, group=group)
+    for byte in (255, 0x7f):
+        fill_free_memory(byte)
+        wb = ck.ck_mx4_weight_prep(w, group)
+        assert all(torch.equal(a, b) for a, b in zip(wb, blocked(*rows)))
+        for m in (1, 40):
+            y = ck.ck_mx4_linear(x[:m], *wb, group=group)
+            assert y.shape == (m, (n + 31) // 32 * 32) and torch.equal(y[:, :n], want[:m]) and not y[:, n:].any()
+        xb = ck.ck_mx4_act_quant(x, group=group)
+        y = ck.ck_mx4_gemm_bf16(*xb, *wb, m=40)
+        assert torch.equal(y[:, :n], want) and not y[:, n:].any()
+        v = ck.ck_mx4_dequant(*wb)
+        assert torch.equal(v[:n, :k].double(), values(*rows)) and not v[n:].any() and not v[:, k:].any()
+
+
+@pytest.mark.parametrize("m", [0, 1, 16, 17, 32, 45])
+@pytest.mark.parametrize("k,group,act", [(64, 1, None), (320, 64, None), (832, 64, "swiglu"), (4096, 128, "swiglu")])
+def test_activation_padding_is_zero(m, k, group, act):
+    x = activation(m, k, 6, act)
+    rows = ck.ck_mx4_act_quant(x, act, group, layout="rows")
+    fill_free_memory(255)
+    xb = ck.ck_mx4_act_quant(x, act, group)
+    if m:   # (the definition above reshapes no empty tensor)
+        assert all(torch.equal(a, b) for a, b in zip(xb, blocked(*rows)))
+    v = ck.ck_mx4_dequant(*xb)
+    want = values(*rows) if m else v[:0, :k].double()
+    assert torch.equal(v[:m, :k].double(), want) and not v[m:].any() and not v[:, k:].any()
