@@ -487,7 +487,8 @@ ck_status ck_mx4_gemm_bf16(const uint8_t *x_codes, const uint8_t *x_scales, cons
                            int64_t m, int64_t n, int64_t k, uint16_t *y, void *stream);
 
 /* The MX FP4 linear: ck_mx4_act_quant of x into the workspace, then
- * ck_mx4_gemm_bf16.  Arguments as there, the weight in CK_LAYOUT_BLOCKED.
+ * ck_mx4_gemm_bf16.  Arguments as there, the weight in CK_LAYOUT_BLOCKED and of
+ * this k (its padded layout does not tell k from another within the same 256).
  *   workspace  ck_mx4_linear_workspace_size(m, k, n) bytes (0: may be NULL),
  *              256-byte aligned, clobbered; apart from every other buffer of the
  *              call.  While m * k, k padded to 256, is at most 16384 (and m at

@@ -764,14 +764,32 @@ def ck_cross_attn(q, k, v, scale=None, kv_len=None, key_mask=None, out=None, wor
 # ---------------------------------------------------------------------------
 # MX FP4 linears: microscaled 4-bit weights and activations
 # ---------------------------------------------------------------------------
+def _mx4_sized(operand, layout, k):
+    """A blocked operand with its k, which the padded shapes do not tell, as an attribute of its codes."""
+    if layout == CK_LAYOUT_BLOCKED:
+        operand[0].in_features = k
+    return operand
+
+
+def _mx4_features(codes, k=None):
+    """The k that an operand's codes or the caller know, or None."""
+    known = getattr(codes, "in_features", None)
+    if k is None:
+        return known
+    if not isinstance(k, int) or known not in (None, k):
+        raise ValueError(f"the weight's codes hold in_features {known}, got k = {k!r}")
+    return k
+
+
 def ck_mx4_weight_prep(w, group: int = 128, layout="blocked"):
     """Rotate and quantize an FP32 weight [n, k] -> (codes, scales), uint8.
     layout "blocked" (default, what the linear reads): codes [n / 32, k / 64,
     1024] and scales [n / 32, k / 256, 256], n padded to 32 and k to 256 with
-    zeros; "rows" (serialized): codes [n, k / 2], the even k in the low nibble, and
+    zeros, codes.in_features the k itself; "rows" (serialized): codes [n, k / 2], the even k in the low nibble, and
     scales [n, k / 32].  group 1: no rotation."""
-    return _done("ck_mx4_weight_prep", (_calls or _native()).mx4_quant(w, CK_ACT_NONE, group, None, _layout_code(layout),
-                                                                      True))
+    lay = _layout_code(layout)
+    return _mx4_sized(_done("ck_mx4_weight_prep", (_calls or _native()).mx4_quant(w, CK_ACT_NONE, group, None, lay, True)),
+                      lay, w.shape[1])
 
 
 def ck_mx4_weight_pack(codes, scales):
@@ -792,15 +810,16 @@ def ck_mx4_weight_pack(codes, scales):
         out_scales = torch.empty((rb, kp // 256, 256), dtype=torch.uint8, device=codes.device)
         _call("ck_mx4_weight_pack", codes.data_ptr(), scales.data_ptr(), n, k, out.data_ptr(), out_scales.data_ptr(),
               _stream(codes))
-    return out, out_scales
+    return _mx4_sized((out, out_scales), CK_LAYOUT_BLOCKED, k)
 
 
 def ck_mx4_act_quant(x, input_act=None, group: int = 128, k: int | None = None, layout="blocked"):
     """Rotate and quantize a BF16 activation [m, columns] (silu(gate) * up of
     [gate | up] with input_act="swiglu") -> (codes, scales) as
     ck_mx4_weight_prep.  The rows may be strided."""
-    return _done("ck_mx4_act_quant", (_calls or _native()).mx4_quant(x, _act_code(input_act), group, k,
-                                                                    _layout_code(layout), False))
+    act, lay = _act_code(input_act), _layout_code(layout)
+    return _mx4_sized(_done("ck_mx4_act_quant", (_calls or _native()).mx4_quant(x, act, group, k, lay, False)), lay,
+                      k if k is not None else x.shape[1] // (2 if act == CK_ACT_SWIGLU else 1))
 
 
 def ck_mx4_dequant(codes, scales, rows: int | None = None, k: int | None = None):
@@ -815,12 +834,15 @@ def ck_mx4_gemm_bf16(x_codes, x_scales, w_codes, w_scales, m: int, n: int | None
     """y = bf16(x w^T (+ bias) (+ residual)) of blocked 4-bit operands with m and
     n logical rows (n default: the weight's padded rows, whose features are zero
     before bias and residual)."""
+    kx, kw = _mx4_features(x_codes), _mx4_features(w_codes)
+    if kx is not None and kw is not None and kx != kw:
+        raise ValueError(f"in_features mismatch: activation {kx}, weight {kw}")
     return _done("ck_mx4_gemm_bf16", (_calls or _native()).mx4_gemm(x_codes, x_scales, w_codes, w_scales, m, n, bias,
                                                                    residual, out))
 
 
 def ck_mx4_linear(x, w_codes, w_scales, n: int | None = None, group: int = 128, input_act=None, out=None,
-                  workspace=None, bias=None, residual=None):
+                  workspace=None, bias=None, residual=None, k: int | None = None):
     """The linear on a 4-bit weight: rotate and quantize x (BF16 [m, k], or
     [m, 2 k] with input_act="swiglu"; rows may be strided), multiply, add the FP32
     bias [n] and the BF16 residual [m, n].
@@ -830,9 +852,12 @@ def ck_mx4_linear(x, w_codes, w_scales, n: int | None = None, group: int = 128, 
     the padding, features that are zero before bias and residual).  `out` may be
     the residual itself and shares no memory with anything else; nor does
     `workspace` (uint8, 256-byte aligned, ck_mx4_linear_workspace_size(m, k, n)
-    bytes)."""
+    bytes).  x must have the weight's k: the codes hold it as their attribute
+    in_features, or it is given as `k` for codes that lost it (a clone, another
+    device); with neither, an x whose k pads to the same multiple of 256 passes."""
     return _done("ck_mx4_linear", (_calls or _native()).mx4_linear(x, w_codes, w_scales, n, group,
-                                                                  _act_code(input_act), bias, residual, out, workspace))
+                                                                  _act_code(input_act), bias, residual, out, workspace,
+                                                                  _mx4_features(w_codes, k)))
 
 
 # ---------------------------------------------------------------------------

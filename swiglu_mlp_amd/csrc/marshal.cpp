@@ -522,11 +522,12 @@ PyObject* mx4_gemm(PyObject*, PyObject* const* a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-// mx4_linear(x, w_codes, w_scales, n, group, act, bias, residual, out, workspace) -> y, or the C status of a refused call
+// mx4_linear(x, w_codes, w_scales, n, group, act, bias, residual, out, workspace, k) -> y, or the C status of a refused
+// call.  k: the weight's in_features, or None where only its padded ones are known.
 PyObject* mx4_linear(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
-    TORCH_CHECK(n == 10 && g_mx4_linear, "mx4_linear: 10 arguments, after bind()");
+    TORCH_CHECK(n == 11 && g_mx4_linear, "mx4_linear: 11 arguments, after bind()");
     const at::Tensor& x = tensor_arg(a[0], "activation");
     const at::Tensor &wc = tensor_arg(a[1], "weight codes"), &ws = tensor_arg(a[2], "weight scales");
     const at::Tensor *bias = optional_arg(a[6], "bias"), *residual = optional_arg(a[7], "residual");
@@ -536,10 +537,13 @@ PyObject* mx4_linear(PyObject*, PyObject* const* a, Py_ssize_t n)
     check_blocked(wc, ws, "the weight", x.device());
     const int64_t m = x.size(0), nn = features_of(a[3], wc), group = PyLong_AsLongLong(a[4]);
     const int act = (int)PyLong_AsLong(a[5]);
+    const bool known = a[10] != Py_None;
+    const int64_t weight_k = known ? PyLong_AsLongLong(a[10]) : 0;
     if (PyErr_Occurred()) return nullptr;
     const int64_t k = act == CK_ACT_SWIGLU ? x.size(1) / 2 : x.size(1);
     TORCH_CHECK_VALUE(act != CK_ACT_SWIGLU || x.size(1) % 2 == 0, "gate and up need one width, got ", x.size(1), " columns");
     check_group(k, group);
+    TORCH_CHECK_VALUE(!known || k == weight_k, "in_features mismatch: activation ", k, ", weight ", weight_k);
     TORCH_CHECK_VALUE(pad(k, 256) == wc.size(1) * 64, "in_features mismatch: activation ", k, ", weight ", wc.size(1) * 64,
                       " (padded to a multiple of 256)");
     bool failed;

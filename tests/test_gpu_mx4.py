@@ -514,3 +514,42 @@ def test_activation_padding_is_zero(m, k, group, act):
     v = ck.ck_mx4_dequant(*xb)
     want = values(*rows) if m else v[:0, :k].double()
     assert torch.equal(v[:m, :k].double(), want) and not v[m:].any() and not v[:, k:].any()
+
+
+def test_in_features_that_pad_to_the_same_width():
+    """A blocked weight is padded to 256 values of k, and its codes say how many they hold."""
+    import copy
+    import io
+    for k, others in ((192, (64, 128, 256)), (256, (64, 192)), (320, (384, 448, 512)), (4096, (4032, 3904))):
+        rows = ck.ck_mx4_weight_prep(torch.randn(48, k, generator=gen(k), device=DEV), 64, layout="rows")
+        prepared = ck.ck_mx4_weight_prep(torch.randn(48, k, generator=gen(k), device=DEV), 64)
+        for wb in (prepared, ck.ck_mx4_weight_pack(*rows)):
+            for act in (None, "swiglu"):
+                for m in (1, 40):
+                    y = ck.ck_mx4_linear(activation(m, k, 3, act), *wb, n=48, group=64, input_act=act)
+                    assert torch.equal(y, ck.ck_mx4_linear(activation(m, k, 3, act), *wb, n=48, group=64, input_act=act, k=k))
+                    for other in others:
+                        x = activation(m, other, 3, act)
+                        with pytest.raises(ValueError):
+                            ck.ck_mx4_linear(x, *wb, n=48, group=64, input_act=act)
+                        with pytest.raises(ValueError):
+                            ck.ck_mx4_linear(x, *wb, n=48, group=64, input_act=act, k=other)
+            for other in others:
+                xb = ck.ck_mx4_act_quant(activation(40, other, 3), group=64)
+                with pytest.raises(ValueError):
+                    ck.ck_mx4_gemm_bf16(*xb, *wb, m=40, n=48)
+            # copies that know it still, and ones that have to be told
+            buf = io.BytesIO()
+            torch.save(wb, buf)
+            buf.seek(0)
+            for again in (copy.deepcopy(wb), torch.load(buf, weights_only=True)):
+                with pytest.raises(ValueError):
+                    ck.ck_mx4_linear(activation(2, others[0], 3), *again, n=48, group=64)
+            bare = [t.clone() for t in wb]
+            x = activation(40, k, 3)
+            assert torch.equal(ck.ck_mx4_linear(x, *bare, n=48, group=64, k=k), ck.ck_mx4_linear(x, *wb, n=48, group=64))
+            for other in others:
+                with pytest.raises(ValueError):
+                    ck.ck_mx4_linear(activation(40, other, 3), *bare, n=48, group=64, k=k)
+    with pytest.raises(ValueError):
+        ck.ck_mx4_linear(x, *bare, n=48, group=64, k=4096.0)
