@@ -879,7 +879,8 @@ def ck_block_norm(x, branch=None, gate=None, residual_scale: float = 1.0, branch
     x, branch: BF16 or FP16 [batch, tokens, width] or [tokens, width], rows may be
     strided.  Norms "rms", "layer" or None, with FP32 weights and biases [width].
     gate, scale, shift: of x's type or all FP32; [width], [batch, width] (a column
-    range of a packed modulation, say) or x's shape.  h is computed from the
+    range of a packed modulation, say) or x's shape, batch or tokens 1 where they
+    share it.  h is computed from the
     unrounded r.  Outputs are new contiguous tensors, or x_out / out, which may be
     x or branch themselves and share no memory with anything else of the call.
     Returns (r, h); h alone without a branch, r alone with norm=None."""

@@ -583,7 +583,8 @@ ck_rows norm_rows(const at::Tensor& t, const char* what, const at::Tensor& x)
     return ck_rows{p, sb, st};
 }
 
-// A modulation [width], [batch, width] (with x [batch, tokens, width]) or x's shape; of x's type or FP32.
+// A modulation [width], [batch, width] (with x [batch, tokens, width]) or x's shape, the dimensions before the width of
+// any size 1; of x's type or FP32.
 ck_rows modulation(const at::Tensor* m, const char* what, const at::Tensor& x, int* dtype)
 {
     if (!m) return ck_rows{};
@@ -596,15 +597,20 @@ ck_rows modulation(const at::Tensor* m, const char* what, const at::Tensor& x, i
     TORCH_CHECK_VALUE(*dtype < 0 || *dtype == mine, "gate, scale and shift need one type");
     *dtype = mine;
     ck_rows r{m->data_ptr(), 0, 0};
-    if (m->sizes() == x.sizes()) {
-        r.batch_stride = x.dim() == 3 && x.size(0) > 1 ? m->stride(0) : 0;
-        r.token_stride = m->size(-2) > 1 ? m->stride(-2) : 0;
-    } else if (m->dim() == 2 && x.dim() == 3 && m->size(0) == x.size(0) && m->size(1) == w) {
+    const int64_t d = m->dim();
+    bool fits = d >= 1 && d <= x.dim() && m->size(d - 1) == w;
+    if (fits && d == x.dim()) {
+        for (int64_t i = 0; i < d - 1; ++i) fits = fits && (m->size(i) == x.size(i) || m->size(i) == 1);
+        if (fits) {
+            r.batch_stride = d == 3 && m->size(0) > 1 ? m->stride(0) : 0;
+            r.token_stride = m->size(d - 2) > 1 ? m->stride(d - 2) : 0;
+        }
+    } else if (fits && d == 2) {
+        fits = m->size(0) == x.size(0);
         r.batch_stride = m->size(0) > 1 ? m->stride(0) : 0;
-    } else {
-        TORCH_CHECK_VALUE(m->dim() == 1 && m->size(0) == w, what, " needs shape (", w, ",)",
-                          x.dim() == 3 ? ", (batch, width)" : "", " or ", x.sizes(), ", got ", m->sizes());
     }
+    TORCH_CHECK_VALUE(fits, what, " needs shape (", w, ",)", x.dim() == 3 ? ", (batch, width)" : "", " or ", x.sizes(),
+                      " with any of the sizes before the width 1, got ", m->sizes());
     const int64_t step = f32 ? 4 : 8;
     TORCH_CHECK_VALUE(m->stride(-1) == 1 && r.batch_stride >= 0 && (r.batch_stride | r.token_stride) % step == 0 &&
                           (uintptr_t)r.data % 16 == 0,

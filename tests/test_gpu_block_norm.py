@@ -343,3 +343,36 @@ def test_block_of_norms_linears_and_attention():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(z, y) and torch.equal(block(x, modulation, rope), y)
+
+
+def test_modulations_of_one_token_or_one_sequence():
+    """[batch, 1, width], as the chunks of a modulation come, and [1, tokens, width]: the same as written out."""
+    g, b, t, w = gen(7), 3, 21, 136
+    x, y = stream(g, b, t, w), torch.randn(b, t, w, generator=g, device=DEV).to(BF16)
+    for mod in (BF16, F32):
+        for shape in ((b, 1, w), (1, t, w), (1, 1, w)):
+            wide = torch.randn(shape[0], shape[1], 6 * w, generator=g, device=DEV).to(mod)
+            gate, scale, shift = (wide[..., i * w:(i + 1) * w] for i in (0, 3, 5))
+            got = check_expanded(x, y, gate, scale, shift)
+            assert all(torch.equal(p, q) for p, q in zip(got, ck.ck_block_norm(
+                x, y, norm="layer", eps=EPS, **{n: m.expand(b, t, w).contiguous() for n, m in
+                                                (("gate", gate), ("scale", scale), ("shift", shift))})))
+    x2, m = x[0], torch.randn(1, w, generator=g, device=DEV)
+    assert torch.equal(ck.ck_block_norm(x2, scale=m, eps=EPS), ck.ck_block_norm(x2, scale=m[0], eps=EPS))
+    for bad in ((b, 2, w), (2, 1, w), (b, 1, w - 8), (1, b, 1, w), (b, t, 1)):
+        with pytest.raises(ValueError):
+            ck.ck_block_norm(x, scale=torch.ones(bad, device=DEV))
+    with pytest.raises(ValueError):     # the channels of every second place
+        ck.ck_block_norm(x, scale=torch.ones(b, 1, 2 * w, device=DEV)[..., ::2])
+    with pytest.raises(ValueError):     # an output that overlaps such a modulation
+        ck.ck_block_norm(x, scale=x[:, :1], out=x)
+
+
+def check_expanded(x, y, gate, scale, shift):
+    """Against the formula, which broadcasts."""
+    r, er, h, eh = reference(x, y, gate.expand(x.shape), norm="layer", scale=scale.expand(x.shape),
+                             shift=shift.expand(x.shape))
+    got = ck.ck_block_norm(x, y, gate=gate, norm="layer", scale=scale, shift=shift, eps=EPS)
+    close(got[0], r, er, x.dtype, (gate.shape, "r"))
+    close(got[1], h, eh, x.dtype, (gate.shape, "h"))
+    return got
