@@ -32,10 +32,13 @@ __device__ __forceinline__ uint32_t scale_byte(float a)
 // 2^(byte - 127), byte < 255 (2^-127 is a subnormal).
 __device__ __forceinline__ float scale_value(uint32_t byte) { return __uint_as_float(max(byte << 23, 0x00400000u)); }
 
-// silu(g) * u for the quantizer.  The hardware's exponential and reciprocal and the
-// rounding of g log2(e) leave it within (4 + |g|) 2^-24 of itself for negative g
-// (4 2^-24 for positive), far below half a step of a 4-bit value.  g = -inf gives
-// NaN (-inf * 0), a large negative g -0.
+// silu(g) * u for the quantizer, within (8 + 1.25 max(-g, 0)) 2^-24 of itself from g =
+// -87 on, far below half a step of a 4-bit value.  In units of 2^-24: the hardware's
+// exponential and reciprocal (1 ulp) 2 each, the sum and the products by g and u 1
+// each; the constant log2(e) 0.23 and the product with it 1, both times |g| as errors
+// of an exponent (for positive g their share e^-g / (1 + e^-g), below 0.28 / g).
+// Below -87, where silu is under 2^-119, the reciprocal is subnormal and then, e^-g
+// past FP32, zero: -0.  g = -inf gives NaN (-inf * 0).
 __device__ __forceinline__ float silu_mul(float g, float u)
 {
     return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -0x1.715476p+0f)) * u;

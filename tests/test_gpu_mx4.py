@@ -553,3 +553,23 @@ def test_in_features_that_pad_to_the_same_width():
                     ck.ck_mx4_linear(activation(40, other, 3), *bare, n=48, group=64, k=k)
     with pytest.raises(ValueError):
         ck.ck_mx4_linear(x, *bare, n=48, group=64, k=4096.0)
+
+
+def test_swiglu_gates():
+    """silu(gate) up without a rotation, gates from -87 to 40 in order, so that a block's are of one size.  In units of
+    2^-24 of the value: the exponential 2, the sum 1, the reciprocal 2, the two products 1 each, and in the exponent log2(e)
+    as a float 0.23 and the product with it 1, each times |gate|, which reach the value by the share e^-g / (1 + e^-g), at
+    most 1 for a negative gate and 0.28 / |gate| for a positive one: (8 + 1.25 max(-gate, 0)) 2^-24."""
+    m, k = 48, 4096
+    g = torch.linspace(-87, 40, m * k, device=DEV).view(m, k).to(BF16)
+    u = torch.randn(m, k, generator=gen(31), device=DEV).to(BF16)
+    u = torch.where(u == 0, 1.0, u)
+    v = (g.double() * torch.sigmoid(g.double()) * u.double()).view(m, k // 32, 32)
+    t = (8 + 1.25 * (-g.double()).clamp(min=0)).view_as(v) * 2.0 ** -24 * v.abs()
+    codes, scales = ck.ck_mx4_act_quant(torch.cat([g, u], 1), "swiglu", 1, layout="rows")
+    s = scales.long()
+    lo, hi = (scale_of((v.abs() + d * t).amax(-1, keepdim=True)) for d in (-1, 1))
+    assert ((s == lo) | (s == hi)).all()
+    unit = torch.exp2(s.double() - 127).unsqueeze(-1)
+    got = values(codes, scales).view_as(v)
+    assert torch.minimum((got - rounded(v - t, unit)).abs(), (got - rounded(v + t, unit)).abs()).max().item() == 0
