@@ -555,6 +555,19 @@ def test_in_features_that_pad_to_the_same_width():
         ck.ck_mx4_linear(x, *bare, n=48, group=64, k=4096.0)
 
 
+# the quantizer in the product's launch: every row count that a workgroup's 512 blocks of 32 allow, rows whose blocks are
+# no multiple of 8, both tile widths with and without SwiGLU, and the first sizes past the limit
+@pytest.mark.parametrize("m,n,k,act,group", [
+    (1, 8208, 2112, "swiglu", 64), (1, 8192, 16384, None, 128), (4, 8192, 4096, "swiglu", 256), (16, 528, 1024, None, 256),
+    (16, 144, 1024, "swiglu", 128), (16, 8240, 64, None, 64), (9, 80, 320, None, 64), (5, 48, 2112, "swiglu", 32),
+    (13, 96, 1088, None, 1), (12, 64, 1280, "swiglu", 256), (17, 80, 64, None, 64), (16, 96, 1088, "swiglu", 64),
+    (2, 48, 8256, None, 64), (1, 8224, 16448, None, 64)])
+def test_linear_in_one_launch(m, n, k, act, group):
+    one = m <= 16 and m * ((k + 255) // 256 * 256) <= 16384
+    assert (ck.lib().ck_mx4_linear_workspace_size(m, k, n) == 0) == one
+    test_linear(m, n, k, act, group)
+
+
 def test_swiglu_gates():
     """silu(gate) up without a rotation, gates from -87 to 40 in order, so that a block's are of one size.  In units of
     2^-24 of the value: the exponential 2, the sum 1, the reciprocal 2, the two products 1 each, and in the exponent log2(e)
