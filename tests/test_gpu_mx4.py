@@ -586,3 +586,19 @@ def test_swiglu_gates():
     unit = torch.exp2(s.double() - 127).unsqueeze(-1)
     got = values(codes, scales).view_as(v)
     assert torch.minimum((got - rounded(v - t, unit)).abs(), (got - rounded(v + t, unit)).abs()).max().item() == 0
+
+
+@pytest.mark.parametrize("m,n,k,act", [(1024, 1024, 1024, None), (4100, 4112, 512, "swiglu"), (530, 4096, 1088, None)])
+def test_linear_whatever_the_memory_held(m, n, k, act):
+    """The same bits from workspaces and outputs that held anything, several tiles a workgroup among them."""
+    x = activation(m, k, 8, act)
+    wb = ck.ck_mx4_weight_prep(torch.randn(n, k, generator=gen(9), device=DEV), 64)
+    room = torch.empty(ck.lib().ck_mx4_linear_workspace_size(m, k, n), dtype=torch.uint8, device=DEV)
+    out = torch.empty(m, n, dtype=BF16, device=DEV)
+    want = None
+    for byte in (0, 255, 0x7f, 0x80, 1):
+        room.fill_(byte)
+        out.view(torch.uint8).fill_(byte)
+        ck.ck_mx4_linear(x, *wb, n=n, group=64, input_act=act, out=out, workspace=room)
+        want = out.clone() if want is None else want
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16))
