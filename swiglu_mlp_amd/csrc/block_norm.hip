@@ -240,7 +240,10 @@ hipError_t launch(const bnorm::Params& p, hipStream_t st)
 // a wave a row (no barriers between the sums, less to wait for) where many rows are
 // narrow.  Measured, wave and workgroup: 16384 rows of 1160 39 and 43 us, 4096 of
 // them 11.4 and 12.2, 1024 5.8 and 5.9, 16 4.9 and 3.7; 16384 rows of 2048 51 and 46;
-// 4096 rows of 4096 34 and 28 (248 registers a lane).
+// 4096 rows of 4096 34 and 28 (248 registers a lane).  Past 8192 channels a workgroup
+// needs 255 or 256 registers a lane, and a SIMD holds two waves (FP16) or one (BF16):
+// 16384 rows of 12288 380 us (4.2 TB/s) and 505 (3.2), of 16384 475 (4.5) and 638
+// (3.4), where rows of 8192 take 195 and 201 (5.4).
 template <typename T, bool NT>
 hipError_t pick_team(const bnorm::Params& p, hipStream_t st)
 {

@@ -8,12 +8,13 @@
 // A k-slice is 64 values, 32 bytes of a row, and one 1 KB block of a 32-row
 // block is an operand in lane order.
 //
-// The matrix cores set the pace of large products: random codes reach 6.5 of
-// the nominal 10 PFLOP/s in a loop of nothing but these instructions (the clock
-// falls under their power).  A wave issues a product every 32 cycles and some 4
-// other instructions in its shadow; past that each one more costs 4 to 8 cycles
-// (measured: 36 cycles a product alone or with 2 scalar ones, 57 with 6, 73 with
-// 8).  So the kernel is built for few instructions a product:
+// The matrix cores set the pace of large products: random codes reach 6.2 to 6.6,
+// by card, of the nominal 10 PFLOP/s in a loop of nothing but these instructions
+// (the clock falls under their power).  A wave issues a product every 32 cycles and
+// some 4 other instructions in its shadow; past that each one more costs 7 or 8 cycles
+// (in a loop, at the nominal clock: 37 cycles a product alone or with 2 scalar ones,
+// 42 with 4, 57 with 6, 73 with 8).  So the kernel is built for few instructions a
+// product:
 //  * A group of 4 waves (2 x 2) owns a BM x BN tile; a wave's part is FM x FN
 //    fragments of 32 x 32, accumulated in AGPRs.  It reads FM + FN blocks from
 //    LDS for FM FN products.
@@ -31,10 +32,11 @@
 //  * Smaller tiles, two groups a workgroup, each with half of k: their waves fill
 //    each other's gaps, and their sums meet in LDS.
 // Small products take mx4_few.hip instead.
-// Measured, cards differing by 4%: 4096 x 4096 -> 24576 191 us (4.3 PFLOP/s; zeros,
-// whose products cost no power, 131 us), 16384 x 12288 -> 4096 333 us (4.95; zeros
-// 219), with a residual of 134 MB 370.  The matrix cores are busy 55 and 62% of the cycles at 1.8 and 1.7 GHz:
-// the power is the limit, and what is not a product there costs energy, not time.
+// Measured, cards differing by 4%: 4096 x 4096 -> 24576 197 to 201 us (4.1 PFLOP/s),
+// 16384 x 12288 -> 4096 331 to 355 us (5.0 to 4.65), with a residual of 134 MB 370 to
+// 382.  The matrix cores are busy 55 and 62% of the cycles at 1.8 and 1.65 GHz.  Codes
+// of zero, whose products cost little power, take 163 and 265 us: a fifth of the time
+// is the power's, the rest beyond the products is the schedule's.
 #include "ck_internal.hpp"
 #include "mx4.hpp"
 #include "mx4_stage.hpp"
@@ -135,8 +137,8 @@ __device__ __forceinline__ void for_each(F&& f)
 template <int BM_, int BN_, int GROUPS_>
 struct Cfg {
     static constexpr int BM = BM_, BN = BN_, GROUPS = GROUPS_;
-    // Pairs of stages in the ring, and stages ahead.  3 and 4 pairs, where they fit,
-    // were no faster (64 x 64 tiles: 7.7 to 7.9 us for 256 x 4096 -> 4096).
+    // Pairs of stages in the ring, and stages ahead (3 and 4 pairs, where they fit, were
+    // no faster).
     static constexpr int R = 2, P = 2 * R - 1;
     static constexpr int FM = BM / 64, FN = BN / 64;    // a wave's fragments
     static constexpr int A_BLK = BN / 16, B_BLK = BM / 16;              // 1 KB blocks of a stage
@@ -406,7 +408,8 @@ __global__ __launch_bounds__(256 * GROUPS) void mx4_gemm_kernel(Args g)
             __builtin_amdgcn_make_buffer_rsrc(g.y + row0 * g.N, (short)0, rows * g.N * 2, 0x00020000);
         const int n_base = tn * BN + wn0 + 8 * lh;
         // The residual's row j is loaded while row j - 1 is stored; the bias, which
-        // every row needs, waits in LDS.
+        // every row needs, waits in LDS.  (Where groups share a tile's rows j0 is no
+        // constant, and in tiles of 128 x 128 these rows lie in scratch, 144 bytes a lane.)
         constexpr int PER_ROW = EXTRA ? C::FN * 2 : 1;
         uint4 res[2][PER_ROW];
         auto load_residual = [&](int j) {
@@ -574,7 +577,7 @@ hipError_t launch(Args g, int num_cu, hipStream_t st)
 
 // Tiles, and what a call on them takes in us: start + rounds (unit + pair pairs), a
 // round being a tile a CU and a pair 256 of k.  The last two are mx4_few.hip's.
-// Measured: 4096 x 4096 -> 24576, 6 rounds of 256 x 256 tiles, 198 us (128 x 256:
+// Measured: 4096 x 4096 -> 24576, 6 rounds of 256 x 256 tiles, 200 us (128 x 256:
 // 226); 2048 x 4096 -> 4096 22 us on 128 x 256 (128 x 128: 28, 256 x 256 on half of
 // the CUs: 28); 1024 x 4096 -> 4096 14 us on 128 x 128 (64 x 128: 19, 128 x 256: 17);
 // 512 x 4096 -> 4096 10.0 us on 64 x 128 (128 x 128: 11.5, 64 x 64: 12.0); 256 x 4096

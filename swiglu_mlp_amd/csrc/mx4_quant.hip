@@ -16,7 +16,7 @@
 // 176).
 //
 // Bound by HBM: 49152 x 4096 BF16 rotated by 128, 510 MB, 80 us (6.4 TB/s); 16384 x
-// 12288 with SwiGLU, 912 MB, 163 us (5.6; without its arithmetic 8 us less); FP32
+// 12288 with SwiGLU, 912 MB, 168 us (5.4; without its arithmetic 8 us less); FP32
 // 12288 x 4096, 228 MB, 46 us (5.0); back to BF16, 127 MB, 19.5 us (6.5); 16 rows
 // 2.2 to 4 us, a launch.
 #include "ck_internal.hpp"
